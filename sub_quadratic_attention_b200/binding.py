@@ -1,10 +1,11 @@
-"""ctypes binding of libspectre_mix (C ABI in include/spectre_mix.h and
-include/dct_mix.h).
+"""ctypes binding of libspectre_mix (C ABI in include/spectre_mix.h,
+include/dct_mix.h, include/gated_scan.h and include/residual_norm.h).
 
 Argument marshalling only: every step of the mix runs in the library's CUDA
-kernels.  The functions carry the C names; :class:`SpectreMix` and
-:class:`DctMix` wrap a handle for use with torch tensors.  Importing this module loads the library and
-raises if it has not been built -- there is no fallback path.
+kernels.  The functions carry the C names; :class:`SpectreMix`, :class:`DctMix`,
+:class:`GatedScan` and :class:`ResidualNorm` wrap a handle for use with torch
+tensors.  Importing this module loads the library and raises if it has not been
+built -- there is no fallback path.
 """
 from __future__ import annotations
 
@@ -43,9 +44,31 @@ SPECTRE_SLICE_TENSOR_CORES = 1
 # fixed device scratch behind spectre_mix_run_noalloc (SPECTRE_NOALLOC_SCRATCH_BYTES)
 SPECTRE_NOALLOC_SCRATCH_BYTES = 64 << 20
 
+GATED_SCAN_GATE = {"sigmoid": 0, "exp": 1}         # enum gated_scan_gate
+GATED_SCAN_PER = {"channel": 0, "head": 1}         # enum gated_scan_per
+GATED_SCAN_CHUNK = 128                             # rows between two saved states
+
 # every entry point the header declares, with its ctypes signature
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
+_ll = ctypes.c_longlong
+_sz = ctypes.c_size_t
+
+
+class GatedScanRows(ctypes.Structure):
+    """struct gated_scan_rows: data, batch stride and row stride (elements)."""
+    _fields_ = [("data", _vp), ("batch_stride", _ll), ("row_stride", _ll)]
+
+
+class GatedScanArgs(ctypes.Structure):
+    """struct gated_scan_args."""
+    _fields_ = [("B", _ll), ("L", _ll), ("cu_seqlens", _vp), ("nseq", _ll),
+                ("g", GatedScanRows), ("v", GatedScanRows), ("y", GatedScanRows),
+                ("dy", GatedScanRows), ("dg", GatedScanRows), ("dv", GatedScanRows),
+                ("h0", _vp), ("hT", _vp), ("dhT", _vp), ("dh0", _vp), ("states", _vp),
+                ("work", _vp), ("work_bytes", _sz), ("zero_outside", _i)]
+
+
 SIGNATURES = {
     "spectre_mix_create": (_i, [ctypes.POINTER(_vp), _i, _i, _i, _i, _i, _i, ctypes.c_float]),
     "spectre_mix_run": (_i, [_vp] * 10),
@@ -65,6 +88,18 @@ SIGNATURES = {
     "dct_mix_run_debug": (_i, [_vp, ctypes.c_longlong] + [_vp] * 4 + [ctypes.c_float] + [_vp] * 5),
     "dct_mix_run_host": (_i, [_vp, ctypes.c_longlong] + [_vp] * 4 + [ctypes.c_float] + [_vp] * 4),
     "dct_mix_destroy": (_i, [_vp]),
+    "gated_scan_create": (_i, [ctypes.POINTER(_vp)] + [_i] * 6),
+    "gated_scan_workspace_bytes": (_sz, [_vp, _ll, _ll, _i]),
+    "gated_scan_run": (_i, [_vp, ctypes.POINTER(GatedScanArgs), _vp]),
+    "gated_scan_backward": (_i, [_vp, ctypes.POINTER(GatedScanArgs), _vp]),
+    "gated_scan_step": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _ll, _vp, _vp]),
+    "gated_scan_destroy": (_i, [_vp]),
+    "residual_norm_create": (_i, [ctypes.POINTER(_vp), _i, _i, _i, ctypes.c_float]),
+    "residual_norm_run": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _ll, _vp]),
+    "residual_norm_workspace_bytes": (_sz, [_vp, _ll]),
+    "residual_norm_backward": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _ll, _vp, _vp,
+                                    _vp, _sz, _vp]),
+    "residual_norm_destroy": (_i, [_vp]),
 }
 
 
@@ -452,6 +487,438 @@ class DctMix:
         if self.handle is not None:
             h, self.handle = self.handle, None
             dct_mix_destroy(h)
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ---------------------------------------------------------------------------
+# operators of rows: the gated linear recurrence (include/gated_scan.h) and the
+# residual norm (include/residual_norm.h)
+# ---------------------------------------------------------------------------
+def _dtype_code(name: str, what: str) -> int:
+    if name in ("f32", "float32", "fp32"):
+        return SPECTRE_F32
+    if name in ("bf16", "bfloat16"):
+        return SPECTRE_BF16
+    raise ValueError(f"{what} must be 'f32' or 'bf16', not {name!r}")
+
+
+def _torch_dtype(code: int):
+    import torch
+
+    return torch.float32 if code == SPECTRE_F32 else torch.bfloat16
+
+
+def _check_tensor(name, t, shape, dtype, device):
+    """A tensor's shape, type and device (``device`` None: any, for host tests)."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {list(shape)} of {dtype}, not {list(t.shape)} of {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the plan on {device}")
+
+
+def _check_plain(name, t, shape, dtype, device):
+    _check_tensor(name, t, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows_of(name, t) -> GatedScanRows:
+    """[B, L, N] as rows: any batch and row stride, the N values contiguous."""
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return GatedScanRows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _row_stride(name, t) -> int:
+    """[..., N] as rows with one stride between them; raises where they have none."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    if t.is_contiguous():
+        return t.shape[-1]
+    stride, extent = None, 1
+    for size, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if stride is None:
+            stride = st
+        elif st != stride * extent:
+            raise ValueError(f"the rows of {name} must have one stride between them")
+        extent *= size
+    return t.shape[-1] if stride is None else stride
+
+
+def _check_outputs(outputs, inputs):
+    """No output may start where an input or another output does."""
+    seen = {t.data_ptr(): name for name, t in inputs if t is not None and t.numel()}
+    for name, t in outputs:
+        if t is None or not t.numel():
+            continue
+        other = seen.setdefault(t.data_ptr(), name)
+        if other != name:
+            raise ValueError(f"{name} may not be the same memory as {other}")
+
+
+def _stream_for(stream, device, tensors) -> int:
+    """The raw stream of a call.  Where it is not the current one, the tensors are
+    marked as in use on it, so that their memory is not handed out again before
+    the work enqueued there is done."""
+    import torch
+
+    current = torch._C._cuda_getCurrentRawStream(device.index)
+    if stream is None:
+        return current
+    raw = stream if isinstance(stream, int) else stream.cuda_stream
+    if raw != current:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+    return raw
+
+
+def gated_scan_create_status(H: int, D: int, gate: int, per: int, dtype: int,
+                             gate_dtype: int) -> Tuple[int, Optional[int]]:
+    h = _vp()
+    code = _lib.gated_scan_create(ctypes.byref(h), H, D, gate, per, dtype, gate_dtype)
+    return code, h.value
+
+
+def gated_scan_create(H: int, D: int, gate: int, per: int, dtype: int, gate_dtype: int) -> int:
+    code, h = gated_scan_create_status(H, D, gate, per, dtype, gate_dtype)
+    _check(code, "gated_scan_create")
+    return h
+
+
+def gated_scan_workspace_bytes(h: Optional[int], B: int, L: int, backward: bool) -> int:
+    return int(_lib.gated_scan_workspace_bytes(h, B, L, int(backward)))
+
+
+def gated_scan_run(h: int, args: GatedScanArgs, stream: int) -> None:
+    _check(_lib.gated_scan_run(h, ctypes.byref(args), stream), "gated_scan_run")
+
+
+def gated_scan_backward(h: int, args: GatedScanArgs, stream: int) -> None:
+    _check(_lib.gated_scan_backward(h, ctypes.byref(args), stream), "gated_scan_backward")
+
+
+def gated_scan_destroy(h: Optional[int]) -> None:
+    _check(_lib.gated_scan_destroy(h), "gated_scan_destroy")
+
+
+def check_scan_sequences(B, L, cu_seqlens, device=None) -> int:
+    """Sequences of a call: B, or those of cu_seqlens (int32 [N + 1], B = 1)."""
+    import torch
+
+    if cu_seqlens is None:
+        return B
+    if B != 1:
+        raise ValueError("packed sequences (cu_seqlens) are rows of one batch entry: B must be 1")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must hold one offset more than sequences")
+    _check_plain("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, device)
+    return cu_seqlens.numel() - 1
+
+
+def check_scan_arguments(H, D, per, dtype_code, gate_code, g, v, device=None, **rows) -> Tuple[int, int]:
+    """Shapes and types of g, v and further tensors of rows (y, dy, dv as v; dg as g);
+    returns (B, L)."""
+    if v.dim() != 3:
+        raise ValueError(f"v must be [B, L, C = {H * D}]")
+    B, L = v.shape[0], v.shape[1]
+    for name, t in dict(g=g, v=v, **rows).items():
+        if t is None:
+            continue
+        gate = name in ("g", "dg")
+        width = H if gate and per == GATED_SCAN_PER["head"] else H * D
+        _check_tensor(name, t, (B, L, width), _torch_dtype(gate_code if gate else dtype_code), device)
+    return B, L
+
+
+class GatedScan:
+    """The gated linear recurrence over [B, L, C = H * D]: a causal token mixer,
+    trained with :meth:`backward` and served token by token with :meth:`step`.
+
+        h_t = a_t h_{t-1} + b_t,  y_t = h_t
+
+    gate="sigmoid": a = sigmoid(g), b = (1 - a) v;  gate="exp": a = exp(g), b = v with
+    log decays g <= 0.  gate_per="channel": g is [B, L, C]; "head": [B, L, H].  v and y
+    are of ``dtype``, g of ``gate_dtype`` ("f32" or the plan's); states are fp32.
+
+    ``scan(g, v)`` returns (y, hT), hT [B, C] the state after the last row.  With
+    ``cu_seqlens`` (int32, N + 1 offsets on the GPU) the L rows of one batch entry are N
+    sequences packed one after another, and states are [N, C]; rows in no sequence are
+    left as they are in tensors that the caller gives, and zero in those made here.
+    For training pass ``states=scan.new_states(B, L)`` to the call and to
+    :meth:`backward`.  g, v and dy may be slices of wider rows; the plan holds nothing
+    of a call, so it may be used on several streams and threads, and inside a graph's
+    capture.  No autograd graph is recorded: backward() is called explicitly.
+    """
+
+    def __init__(self, H: int, D: int, dtype: str = "bf16", gate: str = "sigmoid",
+                 gate_per: str = "channel", gate_dtype: Optional[str] = None):
+        import torch
+
+        self.handle = None
+        if gate not in GATED_SCAN_GATE or gate_per not in GATED_SCAN_PER:
+            raise ValueError("gate must be 'sigmoid' or 'exp', gate_per 'channel' or 'head'")
+        self.H, self.D, self.C = H, D, H * D
+        self.dtype_code = _dtype_code(dtype, "dtype")
+        self.gate_code = self.dtype_code if gate_dtype is None else _dtype_code(gate_dtype, "gate_dtype")
+        self.gate, self.per = GATED_SCAN_GATE[gate], GATED_SCAN_PER[gate_per]
+        self.handle = gated_scan_create(H, D, self.gate, self.per, self.dtype_code, self.gate_code)
+        self.device = torch.device("cuda", torch.cuda.current_device())
+
+    def new_states(self, B: int, L: int):
+        """The tensor that a training forward fills and backward reads: the fp32 state
+        before every GATED_SCAN_CHUNK-th row."""
+        import torch
+
+        return torch.empty((B, -(-L // GATED_SCAN_CHUNK), self.C), dtype=torch.float32, device=self.device)
+
+    def _check_states(self, B, L, nseq, states, **ends):
+        import torch
+
+        if states is not None:
+            _check_plain("states", states, (B, -(-L // GATED_SCAN_CHUNK), self.C), torch.float32, self.device)
+        for name, t in ends.items():
+            if t is not None:
+                _check_plain(name, t, (nseq, self.C), torch.float32, self.device)
+
+    def _work(self, B, L, backward):
+        import torch
+
+        n = gated_scan_workspace_bytes(self.handle, B, L, backward)
+        return torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
+
+    def __call__(self, g, v, h0=None, cu_seqlens=None, y=None, hT=None, states=None, stream=None):
+        import torch
+
+        B, L = check_scan_arguments(self.H, self.D, self.per, self.dtype_code, self.gate_code, g, v,
+                                    self.device, y=y)
+        nseq = check_scan_sequences(B, L, cu_seqlens, self.device)
+        made = y is None
+        if made:
+            y = torch.empty((B, L, self.C), dtype=v.dtype, device=self.device)
+        if hT is None:
+            hT = torch.empty((nseq, self.C), dtype=torch.float32, device=self.device)
+        self._check_states(B, L, nseq, states, h0=h0, hT=hT)
+        _check_outputs([("y", y), ("hT", hT), ("states", states)], [("g", g), ("v", v), ("h0", h0)])
+        work = self._work(B, L, False)
+        a = GatedScanArgs(B=B, L=L, cu_seqlens=_ptr(cu_seqlens), nseq=nseq, g=_rows_of("g", g),
+                          v=_rows_of("v", v), y=_rows_of("y", y), h0=_ptr(h0), hT=_ptr(hT),
+                          states=_ptr(states), work=_ptr(work),
+                          work_bytes=0 if work is None else work.numel(), zero_outside=int(made))
+        gated_scan_run(self.handle, a, _stream_for(stream, self.device,
+                                                   (g, v, h0, cu_seqlens, y, hT, states, work)))
+        return y, hT
+
+    def backward(self, dy, g, v, states, h0=None, dhT=None, cu_seqlens=None, dg=None, dv=None,
+                 dh0=None, stream=None):
+        """(dg, dv, dh0) from dy (and dhT, the gradient of the final states); dh0 is None
+        where h0 is None and no dh0 is given.  ``states`` is what the forward call with the
+        same g, v, h0 and cu_seqlens filled."""
+        import torch
+
+        B, L = check_scan_arguments(self.H, self.D, self.per, self.dtype_code, self.gate_code, g, v,
+                                    self.device, dy=dy, dg=dg, dv=dv)
+        nseq = check_scan_sequences(B, L, cu_seqlens, self.device)
+        if states is None:
+            raise ValueError("backward needs the states that the forward call filled")
+        if (dg is None) != (dv is None):
+            raise ValueError("dg and dv are given together or not at all")
+        made = dg is None
+        if made:
+            dg = torch.empty(g.shape, dtype=g.dtype, device=self.device)
+            dv = torch.empty((B, L, self.C), dtype=v.dtype, device=self.device)
+        if dh0 is None and h0 is not None:
+            dh0 = torch.empty((nseq, self.C), dtype=torch.float32, device=self.device)
+        self._check_states(B, L, nseq, states, h0=h0, dhT=dhT, dh0=dh0)
+        _check_outputs([("dg", dg), ("dv", dv), ("dh0", dh0)],
+                       [("g", g), ("v", v), ("dy", dy), ("h0", h0), ("dhT", dhT), ("states", states)])
+        work = self._work(B, L, True)
+        a = GatedScanArgs(B=B, L=L, cu_seqlens=_ptr(cu_seqlens), nseq=nseq, g=_rows_of("g", g),
+                          v=_rows_of("v", v), dy=_rows_of("dy", dy), dg=_rows_of("dg", dg),
+                          dv=_rows_of("dv", dv), h0=_ptr(h0), dhT=_ptr(dhT), dh0=_ptr(dh0),
+                          states=_ptr(states), work=_ptr(work),
+                          work_bytes=0 if work is None else work.numel(), zero_outside=int(made))
+        gated_scan_backward(self.handle, a,
+                            _stream_for(stream, self.device, (dy, g, v, states, h0, dhT, cu_seqlens,
+                                                              dg, dv, dh0, work)))
+        return dg, dv, dh0
+
+    def step(self, g, v, state, slots=None, y=None, new_state=None, stream=None):
+        """One token of each of B sequences: g [B, C or H], v [B, C], ``state`` the fp32 pool
+        [S, C], ``slots`` (int32 [B]) each row's place in it (None: row i has place i).
+        Returns (y, new_state); new_state is the pool itself, updated in place, unless
+        another tensor is given (its other rows are left as they are).  A row whose slot is
+        outside the pool is skipped: its y is left as it is, or zero where y is made here."""
+        import torch
+
+        B = v.shape[0]
+        width = self.H if self.per == GATED_SCAN_PER["head"] else self.C
+        _check_tensor("g", g, (B, width), _torch_dtype(self.gate_code), self.device)
+        _check_tensor("v", v, (B, self.C), _torch_dtype(self.dtype_code), self.device)
+        if y is None:
+            y = (torch.empty if slots is None else torch.zeros)((B, self.C), dtype=v.dtype, device=self.device)
+        _check_tensor("y", y, (B, self.C), v.dtype, self.device)
+        S = state.shape[0]
+        _check_plain("state", state, (S, self.C), torch.float32, self.device)
+        if new_state is None:
+            new_state = state
+        _check_plain("new_state", new_state, (S, self.C), torch.float32, self.device)
+        if slots is not None:
+            _check_plain("slots", slots, (B,), torch.int32, self.device)
+        elif S < B:
+            raise ValueError(f"state holds {S} rows, the step has {B}")
+        for name, t in (("g", g), ("v", v), ("y", y)):
+            if t.shape[1] > 1 and t.stride(1) != 1:
+                raise ValueError(f"the last dimension of {name} must be contiguous")
+        _check_outputs([("y", y)], [("g", g), ("v", v), ("state", state), ("new_state", new_state)])
+        raw = _stream_for(stream, self.device, (g, v, state, slots, y, new_state))
+        _check(_lib.gated_scan_step(self.handle, B, g.data_ptr(), g.stride(0), v.data_ptr(), v.stride(0),
+                                    state.data_ptr(), S, _ptr(slots), y.data_ptr(), y.stride(0),
+                                    new_state.data_ptr(), raw), "gated_scan_step")
+        return y, new_state
+
+    def close(self) -> None:
+        if self.handle is not None:
+            h, self.handle = self.handle, None
+            gated_scan_destroy(h)
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def residual_norm_create_status(C: int, dtype: int, norm: int, eps: float = 1e-5) -> Tuple[int, Optional[int]]:
+    h = _vp()
+    code = _lib.residual_norm_create(ctypes.byref(h), C, dtype, norm, eps)
+    return code, h.value
+
+
+def residual_norm_create(C: int, dtype: int, norm: int, eps: float = 1e-5) -> int:
+    code, h = residual_norm_create_status(C, dtype, norm, eps)
+    _check(code, "residual_norm_create")
+    return h
+
+
+def residual_norm_workspace_bytes(h: Optional[int], T: int) -> int:
+    return int(_lib.residual_norm_workspace_bytes(h, T))
+
+
+def residual_norm_destroy(h: Optional[int]) -> None:
+    _check(_lib.residual_norm_destroy(h), "residual_norm_destroy")
+
+
+def check_norm_arguments(C, dtype_code, device=None, vectors=(), **rows) -> Tuple[int, ...]:
+    """Shapes and types of a residual norm's tensors: rows [..., C] of the plan's type,
+    all of one shape, and ``vectors`` ((name, tensor), ...) of C fp32 values.  Returns
+    that shape."""
+    import torch
+
+    shape = None
+    for name, t in rows.items():
+        if t is None:
+            continue
+        if shape is None:
+            if t.dim() < 1 or t.shape[-1] != C:
+                raise ValueError(f"{name} must be [..., C = {C}]")
+            shape = tuple(t.shape)
+        _check_tensor(name, t, shape, _torch_dtype(dtype_code), device)
+    for name, t in vectors:
+        if t is not None:
+            _check_plain(name, t, (C,), torch.float32, device)
+    return shape
+
+
+class ResidualNorm:
+    """y = N(out + x) (norm="post_ln", "post_rms") or N(out) + x ("pre_ln", "pre_rms"),
+    N LayerNorm or RMSNorm over the last dimension: the forms that SpectreMix fuses, as an
+    operator of its own with its backward pass.
+
+    ``norm(out, x, gamma, beta)`` takes rows [..., C] and returns y.
+    ``norm.backward(dy, out, x, gamma)`` returns (dout, dx, dgamma, dbeta); dx is dout in
+    the post forms and dy in the pre forms, the same tensor.  Rows may be slices of wider
+    rows.  The plan holds nothing of a call (see GatedScan); no autograd graph is recorded.
+    """
+
+    def __init__(self, C: int, dtype: str = "bf16", norm: str = "post_ln", eps: float = 1e-5):
+        import torch
+
+        self.handle = None
+        if norm not in SPECTRE_NORM:
+            raise ValueError(f"norm must be one of {sorted(SPECTRE_NORM)}, not {norm!r}")
+        self.C, self.eps, self.norm = C, eps, norm
+        self.post = norm.startswith("post")
+        self.dtype_code = _dtype_code(dtype, "dtype")
+        self.handle = residual_norm_create(C, self.dtype_code, SPECTRE_NORM[norm], eps)
+        self.device = torch.device("cuda", torch.cuda.current_device())
+
+    def __call__(self, out, x, gamma, beta, y=None, stream=None):
+        import torch
+
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        check_norm_arguments(self.C, self.dtype_code, self.device, (("gamma", gamma), ("beta", beta)),
+                             out=out, x=x, y=y)
+        _check_outputs([("y", y)], [("out", out), ("x", x)])
+        raw = _stream_for(stream, self.device, (out, x, gamma, beta, y))
+        _check(_lib.residual_norm_run(self.handle, x.numel() // self.C, out.data_ptr(), _row_stride("out", out),
+                                      x.data_ptr(), _row_stride("x", x), gamma.data_ptr(), beta.data_ptr(),
+                                      y.data_ptr(), _row_stride("y", y), raw), "residual_norm_run")
+        return y
+
+    def backward(self, dy, out, x, gamma, dout=None, dgamma=None, dbeta=None, stream=None):
+        import torch
+
+        if self.post and x is None:
+            raise ValueError("the post forms' gradient needs x")
+        if dout is None:
+            dout = torch.empty(out.shape, dtype=out.dtype, device=out.device)
+        if dgamma is None:
+            dgamma = torch.empty(self.C, dtype=torch.float32, device=out.device)
+        if dbeta is None:
+            dbeta = torch.empty(self.C, dtype=torch.float32, device=out.device)
+        check_norm_arguments(self.C, self.dtype_code, self.device,
+                             (("gamma", gamma), ("dgamma", dgamma), ("dbeta", dbeta)),
+                             dy=dy, out=out, x=x, dout=dout)
+        _check_outputs([("dout", dout), ("dgamma", dgamma), ("dbeta", dbeta)],
+                       [("dy", dy), ("out", out), ("x", x), ("gamma", gamma)])
+        T = out.numel() // self.C
+        n = residual_norm_workspace_bytes(self.handle, T)
+        work = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
+        raw = _stream_for(stream, self.device, (dy, out, x, gamma, dout, dgamma, dbeta, work))
+        _check(_lib.residual_norm_backward(
+            self.handle, T, dy.data_ptr(), _row_stride("dy", dy), out.data_ptr(), _row_stride("out", out),
+            x.data_ptr() if self.post else None, _row_stride("x", x) if self.post else 0, gamma.data_ptr(),
+            dout.data_ptr(), _row_stride("dout", dout), dgamma.data_ptr(), dbeta.data_ptr(), _ptr(work), n,
+            raw), "residual_norm_backward")
+        return dout, dout if self.post else dy, dgamma, dbeta
+
+    def close(self) -> None:
+        if self.handle is not None:
+            h, self.handle = self.handle, None
+            residual_norm_destroy(h)
 
     def __enter__(self):
         return self

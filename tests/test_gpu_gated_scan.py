@@ -1,0 +1,519 @@
+"""The gated recurrence on the GPU, forward, backward and step, against the 64-bit reference
+with its derived error bounds (rows_reference.py)."""
+import math
+
+import pytest
+import torch
+
+import rows_reference as ref
+from sub_quadratic_attention_b200 import binding as b
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def _inputs(B, L, H, D, dtype, form, per, gate_dtype=None, seed=0, n=None, slow=False):
+    gen = torch.Generator().manual_seed(seed)
+    C = H * D
+    z = torch.randn(B, L, C if per == "channel" else H, generator=gen)
+    if form == "sigmoid":
+        g = z * 1.5 + (7.0 if slow else 2.0)
+    else:
+        g = -torch.nn.functional.softplus(z) * (0.002 if slow else 0.3)
+    g = g.to(TYPES[gate_dtype or dtype])
+    v, dy = (torch.randn(B, L, C, generator=gen).to(TYPES[dtype]) for _ in range(2))
+    h0, dhT = (torch.randn(n or B, C, generator=gen) for _ in range(2))
+    return g, v, dy, h0, dhT
+
+
+def _cuda(*ts):
+    return [None if t is None else t.cuda() for t in ts]
+
+
+def _check(H, D, dtype, form, per, g, v, dy, h0=None, dhT=None, cu=None, gate_dtype=None, place=None):
+    """Both directions against the reference; ``place`` lays g, v, dy out on the GPU."""
+    B, L, _ = v.shape
+    gd, vd, dyd, h0d, dhTd = _cuda(g, v, dy, h0, dhT)
+    if place:
+        gd, vd, dyd = place(gd, vd, dyd)
+    cud = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+    with b.GatedScan(H, D, dtype, form, per, gate_dtype) as s:
+        states = s.new_states(B, L)
+        y, hT = s(gd, vd, h0=h0d, cu_seqlens=cud, states=states)
+        y2, hT2 = s(gd, vd, h0=h0d, cu_seqlens=cud)
+        dg, dv, dh0 = s.backward(dyd, gd, vd, states, h0=h0d, dhT=dhTd, cu_seqlens=cud)
+        torch.cuda.synchronize()
+    assert torch.equal(y.view(torch.uint8), y2.view(torch.uint8)) and torch.equal(hT.view(torch.uint8), hT2.view(torch.uint8))
+    val, err = ref.scan(g, v, H, D, form, h0, cu, dy, dhT)
+    inside = torch.ones(L, dtype=torch.bool)
+    if cu is not None:
+        inside[:cu[0]] = False
+        inside[cu[-1]:] = False
+    for name, got in (("y", y), ("dg", dg), ("dv", dv)):
+        ref.check(name, got[:, inside], val[name][:, inside], err[name][:, inside])
+        assert not bool(got[:, ~inside].any())      # made by the call: zero outside every sequence
+    ref.check("hT", hT, val["hT"], err["hT"])
+    if h0 is None:
+        assert dh0 is None
+    else:
+        ref.check("dh0", dh0, val["dh0"], err["dh0"])
+    return y, hT, dg, dv, dh0
+
+
+@pytest.mark.parametrize("form", ["sigmoid", "exp"])
+@pytest.mark.parametrize("per", ["channel", "head"])
+@pytest.mark.parametrize("dtype,gate_dtype", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("B,L,H,D", [(2, 37, 2, 16), (1, 300, 3, 20)])
+def test_types_gates_and_layouts(B, L, H, D, dtype, gate_dtype, form, per):
+    g, v, dy, h0, dhT = _inputs(B, L, H, D, dtype, form, per, gate_dtype)
+    _check(H, D, dtype, form, per, g, v, dy, h0, dhT, gate_dtype=gate_dtype)
+
+
+@pytest.mark.parametrize("L", [1, 2, 7, 8, 9, 15, 16, 17, 127, 128, 129, 255, 256, 257, 1000, 5000])
+def test_lengths(L):
+    g, v, dy, h0, dhT = _inputs(2, L, 2, 36, "f32", "sigmoid", "channel", seed=L, slow=True)
+    _check(2, 36, "f32", "sigmoid", "channel", g, v, dy, h0, dhT)
+
+
+@pytest.mark.parametrize("H,D", [(1, 1), (5, 1), (3, 2), (1, 3), (2, 4), (1, 5), (3, 8), (2, 12), (7, 33), (1, 60), (1, 64),
+                                 (2, 68), (1, 100), (3, 128), (1, 130), (1, 257), (2, 320)])
+@pytest.mark.parametrize("per", ["channel", "head"])
+def test_heads(H, D, per):
+    g, v, dy, h0, dhT = _inputs(1, 150, H, D, "bf16", "exp", per, "f32", seed=D)
+    _check(H, D, "bf16", "exp", per, g, v, dy, h0, dhT, gate_dtype="f32")
+
+
+def test_without_initial_state():
+    g, v, dy, _, _ = _inputs(3, 200, 2, 8, "f32", "exp", "head")
+    _check(2, 8, "f32", "exp", "head", g, v, dy)
+
+
+@pytest.mark.parametrize("per", ["channel", "head"])
+@pytest.mark.parametrize("form", ["sigmoid", "exp"])
+def test_long_memory_over_many_chunks(form, per):
+    """Gates near one: the state crosses every chunk border of 9,000 rows."""
+    g, v, dy, h0, dhT = _inputs(1, 9000, 2, 20, "bf16", form, per, "f32", slow=True)
+    _check(2, 20, "bf16", form, per, g, v, dy, h0, dhT, gate_dtype="f32")
+
+
+@pytest.mark.parametrize("cu", [[0, 300], [0, 1, 2, 3, 300], [0, 0, 128, 128, 256, 300, 300], [5, 17, 17, 140, 290],
+                                [0, 127, 129, 299], [300, 300], [0, 0], list(range(0, 301, 3)), [0]])
+@pytest.mark.parametrize("per,dtype", [("channel", "f32"), ("head", "bf16")])
+def test_packed_sequences(cu, per, dtype):
+    """Empty sequences, borders inside and at chunks, rows before the first and behind the last."""
+    g, v, dy, h0, dhT = _inputs(1, 300, 3, 12, dtype, "sigmoid", per, "f32", n=max(1, len(cu) - 1))
+    h0, dhT = h0[:len(cu) - 1], dhT[:len(cu) - 1]
+    _check(3, 12, dtype, "sigmoid", per, g, v, dy, h0, dhT, cu=cu, gate_dtype="f32")
+    _check(3, 12, dtype, "sigmoid", per, g, v, dy, None, None, cu=cu, gate_dtype="f32")
+
+
+def test_rows_outside_the_sequences_are_left_as_they_were():
+    cu = [10, 130, 270]
+    g, v, dy, h0, _ = _inputs(1, 300, 2, 16, "bf16", "exp", "head", n=2)
+    gd, vd, dyd, h0d = _cuda(g, v, dy, h0)
+    cud = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    out = torch.tensor(cu[:1] + cu[-1:]).tolist()
+    with b.GatedScan(2, 16, "bf16", "exp", "head") as s:
+        y, dv = (torch.full((1, 300, 32), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        dg = torch.full((1, 300, 2), 7.0, dtype=torch.bfloat16, device="cuda")
+        states = s.new_states(1, 300)
+        s(gd, vd, h0=h0d, cu_seqlens=cud, y=y, states=states)
+        s.backward(dyd, gd, vd, states, h0=h0d, cu_seqlens=cud, dg=dg, dv=dv)
+        y2, _ = s(gd, vd, h0=h0d, cu_seqlens=cud)
+        torch.cuda.synchronize()
+    for t in (y, dg, dv):
+        assert bool((t[:, :out[0]] == 7).all()) and bool((t[:, out[1]:] == 7).all())
+        assert bool((t[:, out[0]:out[1]] != 7).any())
+    assert torch.equal(y[:, 10:270], y2[:, 10:270])
+
+
+@pytest.mark.parametrize("cu", [[-5, 10, 400], [0, 200, 100, 300], [250, 20], [1000, 2000], [-9, -3]])
+def test_bad_offsets_stay_inside_the_tensors(cu):
+    """Offsets out of range or order: the results are not defined, the neighbouring memory stays."""
+    g, v, dy, h0, _ = _inputs(1, 300, 2, 16, "f32", "exp", "channel", n=len(cu) - 1)
+    gd, vd, dyd, h0d = _cuda(g, v, dy, h0)
+    cud = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    guard = [torch.full((1, 340, 32), 7.0, device="cuda") for _ in range(3)]
+    y, dg, dv = (t[:, 20:320] for t in guard)
+    with b.GatedScan(2, 16, "f32", "exp") as s:
+        states = s.new_states(1, 300)
+        states.zero_()
+        s(gd, vd, h0=h0d, cu_seqlens=cud, y=y, states=states)
+        s.backward(dyd, gd, vd, states, h0=h0d, cu_seqlens=cud, dg=dg, dv=dv)
+        torch.cuda.synchronize()
+    for t in guard:
+        assert bool((t[:, :20] == 7).all()) and bool((t[:, 320:] == 7).all())
+
+
+def _strided(g, v, dy):
+    def wide(t, left, right):
+        big = torch.full(t.shape[:2] + (t.shape[2] + left + right,), float("nan"), dtype=t.dtype, device="cuda")
+        big[..., left:left + t.shape[2]] = t
+        return big[..., left:left + t.shape[2]]
+    return wide(g, 4, 8), wide(v, 3, 2), wide(dy, 0, 5)
+
+
+def _time_major(g, v, dy):
+    return tuple(t.transpose(0, 1).contiguous().transpose(0, 1) for t in (g, v, dy))
+
+
+@pytest.mark.parametrize("place", [_strided, _time_major])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("per", ["channel", "head"])
+def test_strides(place, dtype, per):
+    g, v, dy, h0, dhT = _inputs(3, 140, 2, 12, dtype, "sigmoid", per)
+    _check(2, 12, dtype, "sigmoid", per, g, v, dy, h0, dhT, place=place)
+
+
+def test_halves_of_one_projection_and_of_its_gradient():
+    g, v, dy, h0, _ = _inputs(2, 200, 2, 32, "bf16", "sigmoid", "channel")
+    both = torch.cat([g, v], -1).cuda()
+    gd, vd, dyd = both[..., :64], both[..., 64:], dy.cuda()
+    grad = torch.empty_like(both)
+    with b.GatedScan(2, 32, "bf16") as s:
+        states = s.new_states(2, 200)
+        s(gd, vd, states=states)
+        s.backward(dyd, gd, vd, states, dg=grad[..., :64], dv=grad[..., 64:])
+        dg, dv, _ = s.backward(dyd, gd.contiguous(), vd.contiguous(), states)
+    assert torch.equal(grad, torch.cat([dg, dv], -1))
+
+
+def test_broadcast_inputs():
+    """Stride 0: one gate row for all rows; its gradient comes for every row."""
+    g, v, dy, h0, dhT = _inputs(2, 150, 2, 16, "f32", "exp", "channel")
+    g = g[:1, :1].expand(2, 150, 32)
+    _check(2, 16, "f32", "exp", "channel", g, v, dy, h0, dhT,
+           place=lambda gd, vd, dyd: (gd[:1, :1].expand(2, 150, 32), vd, dyd))
+
+
+@pytest.mark.parametrize("form", ["sigmoid", "exp"])
+@pytest.mark.parametrize("low", [-math.inf, torch.finfo(torch.bfloat16).min])
+def test_gates_of_zero_cut(form, low):
+    """A gate of zero takes out all that lies before it, NaN and infinities included, within a chunk and
+    across chunks; its gradient there is zero."""
+    g, v, dy, h0, dhT = _inputs(1, 600, 1, 16, "bf16", form, "channel")
+    for t in (3, 130, 256, 399, 400):
+        g[:, t] = low
+    clean = v.clone()
+    for t, bad in ((1, math.nan), (129, math.inf), (255, -math.inf), (398, math.nan)):
+        v[:, t] = bad
+    with b.GatedScan(1, 16, "bf16", form) as s:
+        states = s.new_states(1, 600)
+        y, hT = s(g.cuda(), v.cuda(), h0=h0.cuda(), states=states)
+        dg, dv, dh0 = s.backward(dy.cuda(), g.cuda(), v.cuda(), states, h0=h0.cuda())
+        torch.cuda.synchronize()
+    val, err = ref.scan(g, clean, 1, 16, form, h0, None, dy)
+    fine = torch.ones(600, dtype=torch.bool)
+    for lo, hi in ((1, 3), (129, 130), (255, 256), (398, 399)):
+        fine[lo:hi] = False
+        assert not bool(torch.isfinite(y[:, lo:hi]).any())
+    ref.check("y", y[:, fine], val["y"][:, fine], err["y"][:, fine])
+    ref.check("hT", hT, val["hT"], err["hT"])
+    ref.check("dv", dv, val["dv"], err["dv"])
+    ref.check("dh0", dh0, val["dh0"], err["dh0"])
+    ref.check("dg", dg[:, fine], val["dg"][:, fine], err["dg"][:, fine])
+
+
+def test_held_rows():
+    """sigmoid, g = infinity: the state is held whatever stands in v."""
+    g, v, dy, h0, dhT = _inputs(2, 300, 1, 16, "f32", "sigmoid", "channel")
+    held = torch.zeros(300, dtype=torch.bool)
+    held[5:20] = held[120:140] = held[290:] = True
+    g[:, held] = math.inf
+    clean = v.clone()
+    clean[:, held] = 0
+    v[:, held] = math.nan
+    with b.GatedScan(1, 16, "f32") as s:
+        states = s.new_states(2, 300)
+        y, hT = s(g.cuda(), v.cuda(), h0=h0.cuda(), states=states)
+        dg, dv, dh0 = s.backward(dy.cuda(), g.cuda(), v.cuda(), states, h0=h0.cuda(), dhT=dhT.cuda())
+        torch.cuda.synchronize()
+    val, err = ref.scan(g, clean, 1, 16, "sigmoid", h0, None, dy, dhT)
+    for name, got in (("y", y), ("hT", hT), ("dg", dg), ("dv", dv), ("dh0", dh0)):
+        ref.check(name, got, val[name], err[name])
+    assert not bool(dg[:, held].any()) and not bool(dv[:, held].any())
+
+
+def test_nan_stays_in_its_channel_sequence_and_future():
+    g, v, dy, h0, _ = _inputs(1, 300, 1, 16, "f32", "exp", "channel", n=3, slow=True)
+    v[0, 140, 3] = math.nan
+    cu = [0, 100, 200, 300]
+    with b.GatedScan(1, 16, "f32", "exp") as s:
+        cud = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        states = s.new_states(1, 300)
+        y, hT = s(g.cuda(), v.cuda(), cu_seqlens=cud, states=states)
+        dg, dv, _ = s.backward(dy.cuda(), g.cuda(), v.cuda(), states, cu_seqlens=cud)
+        torch.cuda.synchronize()
+    want = torch.zeros(1, 300, 16, dtype=torch.bool)
+    want[0, 140:200, 3] = True
+    assert torch.equal(torch.isnan(y).cpu(), want)
+    assert torch.isnan(hT).cpu().nonzero().tolist() == [[1, 3]]
+    assert not bool(torch.isnan(dv).any())
+    want[0, 140, 3] = False     # its own gate's slope is the state before it
+    assert torch.equal(torch.isnan(dg).cpu(), want)
+
+
+def test_empty_calls():
+    with b.GatedScan(2, 8, "bf16", gate_per="head") as s:
+        for B, L in ((0, 5), (2, 0), (0, 0)):
+            g = torch.empty(B, L, 2, dtype=torch.bfloat16, device="cuda")
+            v = torch.empty(B, L, 16, dtype=torch.bfloat16, device="cuda")
+            h0 = torch.randn(B, 16, device="cuda")
+            st = s.new_states(B, L)
+            y, hT = s(g, v, h0=h0, states=st)
+            assert y.shape == v.shape and torch.equal(hT, h0)
+            _, hT = s(g, v)
+            assert torch.equal(hT, torch.zeros_like(h0))
+            dg, dv, dh0 = s.backward(v, g, v, st, h0=h0, dhT=h0 * 2)
+            assert dg.shape == g.shape and dv.shape == v.shape and torch.equal(dh0, h0 * 2)
+        pool = torch.randn(3, 16, device="cuda")
+        keep = pool.clone()
+        e = torch.empty(0, 2, dtype=torch.bfloat16, device="cuda"), torch.empty(0, 16, dtype=torch.bfloat16, device="cuda")
+        y, new = s.step(*e, pool)
+        assert y.shape == (0, 16) and torch.equal(new, keep)
+
+
+@pytest.mark.parametrize("form", ["sigmoid", "exp"])
+@pytest.mark.parametrize("per", ["channel", "head"])
+@pytest.mark.parametrize("dtype,gate_dtype", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("B,H,D", [(1, 1, 1), (3, 2, 16), (5, 7, 33), (2, 3, 130)])
+def test_step(B, H, D, dtype, gate_dtype, form, per):
+    """The step is a sequence of one row from the pool's state."""
+    g, v, _, _, _ = _inputs(B, 1, H, D, dtype, form, per, gate_dtype)
+    pool = torch.randn(B + 3, H * D, generator=torch.Generator().manual_seed(1))
+    slots = torch.randperm(B + 3, generator=torch.Generator().manual_seed(2))[:B].int()
+    val, err = ref.scan(g, v, H, D, form, pool[slots.long()])
+    with b.GatedScan(H, D, dtype, form, per, gate_dtype) as s:
+        p = pool.cuda()
+        y, new = s.step(g[:, 0].cuda(), v[:, 0].cuda(), p, slots=slots.cuda())
+        assert new is p
+        kept = pool.cuda()
+        other = torch.full_like(kept, 7.0)
+        y2, new2 = s.step(g[:, 0].cuda(), v[:, 0].cuda(), kept, slots=slots.cuda(), new_state=other)
+        y3, new3 = s.step(g[:, 0].cuda(), v[:, 0].cuda(), pool[slots.long()].cuda())
+        torch.cuda.synchronize()
+    ref.check("y", y[:, None], val["y"], err["y"])
+    ref.check("state", new[slots.long().cuda()], val["hT"], err["hT"])
+    rest = torch.ones(B + 3, dtype=torch.bool)
+    rest[slots.long()] = False
+    assert torch.equal(new[rest.cuda()].cpu(), pool[rest]) and bool((new2[rest.cuda()] == 7).all())
+    assert torch.equal(kept.cpu(), pool) and torch.equal(y, y2) and torch.equal(y, y3)
+    assert torch.equal(new2[slots.long().cuda()], new3) and torch.equal(new[slots.long().cuda()], new3)
+
+
+def test_step_slots_out_of_range_and_repeated():
+    """Rows without a place are skipped; rows of one place are taken in order, as a sequence."""
+    g, v, _, _, _ = _inputs(1, 9, 2, 36, "f32", "sigmoid", "channel")
+    slots = torch.tensor([2, -1, 2, 4, 0, 5, 2, 0, 2 ** 31 - 1], dtype=torch.int32)
+    pool = torch.randn(5, 72, generator=torch.Generator().manual_seed(1))
+    for separate in (False, True):
+        with b.GatedScan(2, 36, "f32") as s:
+            y = torch.full((9, 72), 7.0, device="cuda")
+            p = pool.cuda()
+            new = torch.full_like(p, 7.0) if separate else p
+            s.step(g[0].cuda(), v[0].cuda(), p, slots=slots.cuda(), y=y, new_state=new)
+            made, _ = s.step(g[0].cuda(), v[0].cuda(), pool.cuda(), slots=slots.cuda())
+            torch.cuda.synchronize()
+        for slot in range(5):
+            rows = (slots == slot).nonzero()[:, 0]
+            if not len(rows):
+                assert torch.equal(new[slot].cpu(), torch.full((72,), 7.0) if separate else pool[slot])
+                continue
+            val, err = ref.scan(g[:, rows], v[:, rows], 2, 36, "sigmoid", pool[slot:slot + 1])
+            ref.check("y", y[rows.cuda()][None], val["y"], err["y"])
+            ref.check("state", new[slot:slot + 1], val["hT"], err["hT"])
+        skipped = ((slots < 0) | (slots >= 5)).cuda()
+        assert bool((y[skipped] == 7).all()) and not bool(made[skipped].any())
+
+
+def test_prefill_then_steps_is_one_scan():
+    g, v, _, h0, _ = _inputs(2, 140, 2, 16, "f32", "exp", "head")
+    val, err = ref.scan(g, v, 2, 16, "exp", h0)
+    gd, vd, h0d = _cuda(g, v, h0)
+    with b.GatedScan(2, 16, "f32", "exp", "head") as s:
+        y, state = s(gd[:, :131], vd[:, :131], h0=h0d)
+        rest = [s.step(gd[:, t], vd[:, t], state)[0] for t in range(131, 140)]
+        torch.cuda.synchronize()
+    ref.check("y", torch.cat([y, torch.stack(rest, 1)], 1), val["y"], err["y"])
+    ref.check("hT", state, val["hT"], err["hT"])
+
+
+def test_large_step_batch():
+    """More rows than a grid's y extent."""
+    B = 70000
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    g, v = (torch.randn(B, 4, generator=gen, device="cuda") for _ in range(2))
+    state = torch.randn(B, 4, generator=gen, device="cuda")
+    with b.GatedScan(1, 4, "f32") as s:
+        y, new = s.step(g, v, state, new_state=torch.empty_like(state))
+    a = torch.sigmoid(g.double())
+    want = a * state.double() + (1 - a) * v.double()
+    assert bool(((new.double() - want).abs() <= ref.K * ref.U * (state.double().abs() + v.double().abs())).all())
+    assert torch.equal(y, new)
+
+
+def test_offsets_beyond_32_bits():
+    """Rows whose element offsets pass 2^31 through their strides."""
+    L, C, stride = 260, 8, 1 << 23          # 260 rows of 2^23 elements apart: 2.18e9 elements, bf16
+    big = torch.empty(L * stride, dtype=torch.bfloat16, device="cuda")
+    g, v, dy, h0, dhT = _inputs(1, L, 1, C, "bf16", "exp", "channel", slow=True)
+    vd = big.as_strided((1, L, C), (L * stride, stride, 1))
+    yd = big.as_strided((1, L, C), (L * stride, stride, 1), 64)
+    vd.copy_(v)
+    with b.GatedScan(1, C, "bf16", "exp") as s:
+        st = s.new_states(1, L)
+        _, hT = s(g.cuda(), vd, h0=h0.cuda(), y=yd, states=st)
+        dvd = big.as_strided((1, L, C), (L * stride, stride, 1), 128)
+        dg = torch.empty_like(g, device="cuda")
+        s.backward(dy.cuda(), g.cuda(), vd, st, h0=h0.cuda(), dhT=dhT.cuda(), dg=dg, dv=dvd)
+        torch.cuda.synchronize()
+    val, err = ref.scan(g, v, 1, C, "exp", h0, None, dy, dhT)
+    ref.check("y", yd, val["y"], err["y"])
+    ref.check("dv", dvd, val["dv"], err["dv"])
+    ref.check("dg", dg, val["dg"], err["dg"])
+
+
+def test_equal_inputs_give_equal_bits():
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    g = torch.randn(1, 40000, 128, generator=gen, device="cuda").add_(5).bfloat16()
+    v, dy = (torch.randn(1, 40000, 128, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    runs = []
+    with b.GatedScan(2, 64, "bf16") as s:
+        for _ in range(6):
+            st = s.new_states(1, 40000)
+            out = s(g, v, states=st)
+            runs.append([*out, st, *s.backward(dy, g, v, st)[:2]])
+    for other in runs[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(runs[0], other))
+
+
+def test_streams_and_two_calls_at_once():
+    """One plan on two streams at a time, each call with its own workspace."""
+    g, v, dy, h0, _ = _inputs(1, 3000, 2, 32, "f32", "sigmoid", "channel", slow=True)
+    gd, vd, dyd = _cuda(g, v, dy)
+    with b.GatedScan(2, 32, "f32") as s:
+        st0 = s.new_states(1, 3000)
+        want = [*s(gd, vd, states=st0), *s.backward(dyd, gd, vd, st0)[:2]]
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in range(3)]
+        got = []
+        for i in range(12):
+            st = s.new_states(1, 3000)
+            q = streams[i % 3]
+            q.wait_stream(torch.cuda.current_stream())
+            handle = q if i % 2 else q.cuda_stream
+            out = s(gd, vd, states=st, stream=handle)
+            got.append([*out, *s.backward(dyd, gd, vd, st, stream=handle)[:2]])
+        torch.cuda.synchronize()
+    for one in got:
+        assert all(torch.equal(x, y) for x, y in zip(want, one))
+
+
+def test_captured_graphs():
+    """Two graphs of one plan, replayed on two streams with new inputs."""
+    g, v, dy, h0, _ = _inputs(1, 2000, 2, 32, "bf16", "exp", "head", slow=True)
+    with b.GatedScan(2, 32, "bf16", "exp", "head") as s:
+        graphs, outs, ins = [], [], []
+        for i in range(2):
+            gd, vd, dyd = _cuda(g, v, dy)
+            st = s.new_states(1, 2000)
+            s(gd, vd, states=st)
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                out = [*s(gd, vd, states=st)]
+                out += s.backward(dyd, gd, vd, st)[:2]
+            graphs.append(graph)
+            outs.append(out)
+            ins.append((gd, vd, dyd))
+        for seed in (5, 6):
+            sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+            new = [_cuda(*_inputs(1, 2000, 2, 32, "bf16", "exp", "head", seed=seed + 10 * i, slow=True)[:3]) for i in range(2)]
+            for i in range(2):
+                for old, n in zip(ins[i], new[i]):
+                    old.copy_(n)
+            torch.cuda.synchronize()
+            for i in range(2):
+                with torch.cuda.stream(sides[i]):
+                    graphs[i].replay()
+            torch.cuda.synchronize()
+            for i in range(2):
+                st = s.new_states(1, 2000)
+                want = [*s(new[i][0], new[i][1], states=st)]
+                want += s.backward(new[i][2], new[i][0], new[i][1], st)[:2]
+                assert all(torch.equal(x, y) for x, y in zip(outs[i], want))
+        del graphs
+
+
+def test_gradient_against_differences():
+    """The kernels' gradients against central differences of the 64-bit forward pass; the gradients' bound is the
+    reference's, the differences' own error about 1e-9."""
+    H, D, L = 2, 4, 140
+    g, v, dy, h0, dhT = _inputs(1, L, H, D, "f32", "sigmoid", "head")
+    val, err = ref.scan(g, v, H, D, "sigmoid", h0, None, dy, dhT)
+    with b.GatedScan(H, D, "f32", "sigmoid", "head") as s:
+        st = s.new_states(1, L)
+        s(g.cuda(), v.cuda(), h0=h0.cuda(), states=st)
+        dg, dv, dh0 = s.backward(dy.cuda(), g.cuda(), v.cuda(), st, h0=h0.cuda(), dhT=dhT.cuda())
+        torch.cuda.synchronize()
+
+    def loss(p):
+        o, _ = ref.scan(p["g"], p["v"], H, D, "sigmoid", p["h0"])
+        return float((dy.double() * o["y"]).sum() + (dhT.double() * o["hT"]).sum())
+
+    p = {"g": g.double(), "v": v.double(), "h0": h0.double()}
+    for name, got, places in (("g", dg, (0, 5, 130, 270)), ("v", dv, (0, 9, 513, 1100)), ("h0", dh0, (0, 7))):
+        for at in places:
+            d = torch.zeros(p[name].numel(), dtype=torch.float64)
+            d[at] = 1e-5
+            d = d.view_as(p[name])
+            diff = (loss({**p, name: p[name] + d}) - loss({**p, name: p[name] - d})) / 2e-5
+            limit = err["d" + name].reshape(-1)[at].item() + 1e-7
+            assert abs(got.reshape(-1)[at].item() - diff) <= limit
+
+
+def test_refusals():
+    g, v, dy, h0, _ = _inputs(2, 20, 2, 8, "bf16", "exp", "channel")
+    gd, vd, dyd, h0d = _cuda(g, v, dy, h0)
+    with b.GatedScan(2, 8, "bf16", "exp") as s:
+        st = s.new_states(2, 20)
+        for bad in (dict(g=g, v=vd), dict(g=gd, v=vd, h0=h0d[:1]), dict(g=gd, v=vd, h0=h0d.double()),
+                    dict(g=gd, v=vd, y=vd), dict(g=gd, v=vd, y=gd), dict(g=gd, v=vd, states=st[:, :0]),
+                    dict(g=gd, v=vd, hT=h0d, h0=h0d), dict(g=gd.transpose(1, 2), v=vd),
+                    dict(g=gd, v=vd, cu_seqlens=torch.tensor([0, 20], dtype=torch.int32, device="cuda"))):
+            with pytest.raises(ValueError):
+                s(**bad)
+        for bad in (dict(states=None), dict(states=st, dg=torch.empty_like(gd)), dict(states=st, dg=gd, dv=vd)):
+            with pytest.raises(ValueError):
+                s.backward(dyd, gd, vd, **bad)
+        with pytest.raises(b.SpectreMixError) as e:      # rows that overlap
+            s(gd, vd, y=torch.empty(2, 1, 16, dtype=torch.bfloat16, device="cuda").expand(2, 20, 16))
+        assert e.value.code == b.SPECTRE_ERR_ARG
+        pool = torch.zeros(1, 16, device="cuda")
+        with pytest.raises(ValueError):
+            s.step(gd[:, 0], vd[:, 0], pool)
+        with pytest.raises(ValueError):
+            s.step(gd[:, 0], vd[:, 0], pool, slots=torch.zeros(2, device="cuda"))
+        with pytest.raises(ValueError):
+            s.step(gd[:, 0], vd[:, 0], torch.zeros(2, 16, device="cuda"), y=vd[:, 0])
+        # the C entry points: short or misaligned workspaces, misaligned rows
+        a = b.GatedScanArgs(B=2, L=20, g=b.GatedScanRows(gd.data_ptr() + 1, 320, 16), v=b._rows_of("v", vd),
+                            y=b._rows_of("y", torch.empty_like(vd)))
+        assert b._lib.gated_scan_run(s.handle, a, None) == b.SPECTRE_ERR_ALIGN
+        a.g.data = gd.data_ptr()
+        a.B = -1
+        assert b._lib.gated_scan_run(s.handle, a, None) == b.SPECTRE_ERR_ARG
+        a.B, a.L = 1 << 40, 1 << 40
+        assert b._lib.gated_scan_run(s.handle, a, None) == b.SPECTRE_ERR_ARG
+    with b.GatedScan(2, 160, "f32", "exp", "head") as s:
+        need = b.gated_scan_workspace_bytes(s.handle, 1, 4, True)
+        t = [torch.zeros(1, 4, n, device="cuda") for n in (2, 320, 320, 2, 320)]
+        st = s.new_states(1, 4)
+        work = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
+        r = [b._rows_of("t", x) for x in t]
+        a = b.GatedScanArgs(B=1, L=4, g=r[0], v=r[1], dy=r[2], dg=r[3], dv=r[4], states=st.data_ptr(),
+                            work=work.data_ptr(), work_bytes=need - 1)
+        assert b._lib.gated_scan_backward(s.handle, a, None) == b.SPECTRE_ERR_ARG
+        a.work, a.work_bytes = work.data_ptr() + 4, need
+        assert b._lib.gated_scan_backward(s.handle, a, None) == b.SPECTRE_ERR_ALIGN
