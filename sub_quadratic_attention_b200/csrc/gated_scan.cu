@@ -18,16 +18,21 @@
 //
 // Looking back.  A tile's pair is one 64-bit word in memory, written whole: readers need
 // neither a flag nor a fence.  It is first (P, Q) and, when the state before the tile is
-// known, (0, state behind it): a stretch that lets nothing through.  A reader goes back to
-// the nearest pair with P = 0 and applies the pairs from there on in order, which is the
+// known, (0, state behind it): a stretch that lets nothing through.  A reader takes the
+// nearest pair with P = 0 and applies the pairs from there on in order, which is the
 // arithmetic that the tiles between do themselves: the result is the same to the bit
-// whichever of the two words it meets.  Tiles take their number from a counter, so the
-// tiles that a waiting block looks at are held by blocks that run already.  A wait that
-// finds nothing for about four seconds ends with NaN in the state and in all rows behind.
+// whichever of the two words it meets.  The blocks are launched together and take the tiles
+// in order, so the tiles that a waiting block looks at are done or being worked on.  A wait
+// that finds nothing for some seconds ends with NaN in the state and in all rows behind.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <new>
+#include <type_traits>
 
 #include "gated_scan.h"
 #include "rows_io.cuh"
+#include "tc_dft.cuh"
 
 struct gated_scan_s {
     int H, D, C;
@@ -46,24 +51,46 @@ struct Gate {
     float a, c;   // h = a h + c v
 };
 
-// A gate in one number.  exp: a itself.  sigmoid: the smaller of a = s(g) and 1 - a = s(-g),
-// e / (1 + e) with e = exp(-|g|), to its own relative precision, with g's sign to tell which;
-// the other is one minus it, exact to half a step since it is at least a half.
-template <int FORM> __device__ __forceinline__ float pack_gate(float g) {
-    if (FORM == GATED_SCAN_EXP) return expf(g);
-    const float e = expf(-fabsf(g));
-    return copysignf(e / (1.0f + e), g);
+// The smaller of a = s(g) and 1 - a = s(-g) is e / (1 + e) with e = exp(-|g|), to its own
+// relative precision; the larger is one minus it, off by at most half a step of one, so that
+// a decay close to one stays as exact as its distance from one.  bf16 rows take the hardware's
+// exp2 and reciprocal (a few units of 2^-24 of the smaller factor, far below the rows' own
+// rounding); a log decay's exp is the accurate one for every type, since its error adds up
+// over as many rows as the state lasts.
+template <int FORM, bool FAST> __device__ __forceinline__ Gate gate_of(float g) {
+    if (FORM == GATED_SCAN_EXP) return {expf(g), 1.0f};
+    float s;
+    if (FAST) {
+        const float e = __expf(-fabsf(g));
+        s = __fdividef(e, 1.0f + e);
+    } else {
+        const float e = expf(-fabsf(g));
+        s = e / (1.0f + e);
+    }
+    const float o = 1.0f - s;
+    return g >= 0.0f ? Gate{o, s} : Gate{s, o};
+}
+// The same gate in one number: a log decay's a, or the smaller factor with g's sign.
+template <int FORM, bool FAST> __device__ __forceinline__ float pack_gate(float g) {
+    const Gate k = gate_of<FORM, FAST>(g);
+    return FORM == GATED_SCAN_EXP ? k.a : copysignf(g >= 0.0f ? k.c : k.a, g);
 }
 template <int FORM> __device__ __forceinline__ Gate open_gate(float k) {
     if (FORM == GATED_SCAN_EXP) return {k, 1.0f};
     const float s = fabsf(k), o = 1.0f - s;
     return signbit(k) ? Gate{s, o} : Gate{o, s};
 }
-template <int FORM> constexpr float HOLD = FORM == GATED_SCAN_EXP ? 1.0f : 0.0f;   // a = 1
+template <int FORM> constexpr float HOLD = FORM == GATED_SCAN_EXP ? 1.0f : 0.0f;   // packed: a = 1
 
 // a * h where a factor of zero takes h out, NaN and infinities included
 __device__ __forceinline__ float mul0(float a, float h) { return a == 0.0f ? 0.0f : a * h; }
 __device__ __forceinline__ float fma0(float a, float h, float b) { return a == 0.0f ? b : fmaf(a, h, b); }
+// the same where h is known to be finite, or where NaN only tells that it was not
+template <bool GUARD> __device__ __forceinline__ float fma_if(float a, float h, float b) {
+    return GUARD ? fma0(a, h, b) : fmaf(a, h, b);
+}
+template <bool GUARD> __device__ __forceinline__ float mul_if(float a, float h) { return GUARD ? mul0(a, h) : a * h; }
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < __int_as_float(0x7f800000); }
 
 template <int FORM> __device__ __forceinline__ float input_of(Gate k, float v) {
     return FORM == GATED_SCAN_EXP ? v : mul0(k.c, v);
@@ -74,30 +101,28 @@ template <int FORM> __device__ __forceinline__ float slope_of(Gate k, float befo
 }
 
 
-// A tile: CHUNK rows of WIDTH channels.  V channels a thread: 4 where rows and heads allow it,
-// else 1 (then a row's part is 32 channels and a thread has 16 rows).
-template <int V> struct Tile {
-    static constexpr int LANES = V == 4 ? 16 : 32;
+// A tile: CHUNK rows of WIDTH channels, 128 bytes of a row.  V channels a thread: 4 where rows and
+// heads allow it, else 1 (then a row's part is 32 channels and a thread has 16 rows).
+template <typename TV, int V> struct Tile {
+    static constexpr int LANES = V == 4 ? 128 / (4 * (int)sizeof(TV)) : 32;
     static constexpr int WIDTH = LANES * V;
     static constexpr int ROWS = V == 4 ? 8 : 16;
     static constexpr int GROUPS = CHUNK / ROWS;
     static constexpr int THREADS = LANES * GROUPS;
 };
 
-// Workspace: a counter and one word for each tile and channel, all ones before a run.
-constexpr size_t COUNTER_BYTES = 256;
+// Workspace: one word for each tile and channel, all ones before a run.
 constexpr unsigned long long NOTHING = ~0ull;
-constexpr int WINDOW = 8;              // pairs that a reader asks for at a time
-constexpr unsigned MOST_POLLS = 1u << 22;   // about a microsecond each
+constexpr unsigned MOST_POLLS = 1u << 22;   // of about a microsecond each
 
 struct Args {
     gated_scan_args a;
     int H, D, C;
     int strips;               // tiles beside one another: ceil(C / WIDTH)
     int nchunk;
+    int nsm;
     long long nseq;           // dense: B
-    unsigned *counter;        // null where a sequence has one chunk
-    unsigned long long *words;
+    unsigned long long *words;   // null where a sequence has one chunk
     float *parts;             // per-head gradients of heads that span strips: [pieces][B L][H]
 };
 
@@ -132,49 +157,59 @@ __device__ __forceinline__ void publish(unsigned long long *p, float P, float Q)
 __device__ __forceinline__ float word_P(unsigned long long w) { return __uint_as_float((unsigned)(w >> 32)); }
 __device__ __forceinline__ float word_Q(unsigned long long w) { return __uint_as_float((unsigned)w); }
 
-// The state in front of tile i (counted in the direction of the walk) of a strip's channel:
-// words[j * WIDTH] is tile j's.  Tile 0's word has P = 0.
-template <int WIDTH> __device__ float look_back(const unsigned long long *words, int i) {
-    int found = -1;
-    float state = 0.0f;
-    unsigned polls = 0;
-    for (int last = i - 1; found < 0;) {
-        unsigned long long w[WINDOW];
+// The state in front of tile i (counted in the direction of the walk) of a strip, for each of its
+// channels, found by the whole block: words[j * WIDTH + x] is tile j's word for channel x, and tile
+// 0's has P = 0.  Thread (q, x) asks for the REACH words at distances q * REACH + 1 and on, of
+// every q at once or, where the tiles in flight are few, of q = 0 first.  A channel is done when the
+// nearest word with P = 0 is among them and nothing is missing before it; tiles ahead that are not
+// done will be, so a block that finds no such word asks again instead of going further back.
+constexpr int REACH = 8;
+template <int WIDTH, int QS> struct LookBack {
+    float state[WIDTH];
+    unsigned char seen[QS][WIDTH];
+};
+template <int WIDTH, int QS>
+__device__ __forceinline__ void look_back(LookBack<WIDTH, QS> &m, const unsigned long long *words, int i, bool mine, bool far) {
+    const int x = threadIdx.x % WIDTH, q = threadIdx.x / WIDTH;
+    unsigned long long w[REACH];
+    for (unsigned polls = 0;; polls++) {
+        const int qs = far || polls ? QS : 1;
+        if (q < qs) {
+            const int last = i - 1 - q * REACH;
 #pragma unroll
-        for (int j = 0; j < WINDOW; j++) w[j] = last - j >= 0 ? peek(words + (long long)(last - j) * WIDTH) : 0;
-        int from = -1;      // the nearest tile of this window that lets nothing through
-        bool wait = false;
+            for (int j = 0; j < REACH; j++) w[j] = mine && last - j >= 0 ? peek(words + (long long)(last - j) * WIDTH + x) : 0;
+            int seen = REACH;       // how many pairs come before a word with P = 0; one more: a word is missing
 #pragma unroll
-        for (int j = 0; j < WINDOW; j++) {
-            if (from >= 0 || wait) continue;
-            if (w[j] == NOTHING)
-                wait = true;
-            else if (word_P(w[j]) == 0.0f)
-                from = j;
+            for (int j = REACH - 1; j >= 0; j--) {
+                if (w[j] == NOTHING)
+                    seen = REACH + 1;
+                else if (word_P(w[j]) == 0.0f)
+                    seen = j;
+            }
+            m.seen[q][x] = (unsigned char)seen;
         }
-        if (wait) {
-            if (++polls > MOST_POLLS) return __uint_as_float(0x7fc00000u);
-            continue;
+        __syncthreads();
+        int from = 0, at = REACH;   // the word with P = 0: thread from's number at
+        while (from < qs && (at = m.seen[from][x]) == REACH) from++;
+        if (__syncthreads_or(at >= REACH)) {
+            if (polls < MOST_POLLS) continue;
+            if (q == 0) m.state[x] = __uint_as_float(0x7fc00000u);
+            __syncthreads();
+            return;
         }
-        if (from < 0) {
-            last -= WINDOW;
-            continue;
-        }
+        // from the farthest word on, in order
+        for (int k = __syncthreads_or(from > 0) ? qs - 1 : 0; k >= 0; k--) {
+            if (q == k && k <= from) {
+                float state = k == from ? 0.0f : m.state[x];
 #pragma unroll
-        for (int j = WINDOW - 1; j >= 0; j--)
-            if (j <= from) state = fma0(word_P(w[j]), state, word_Q(w[j]));
-        found = last;
+                for (int j = REACH - 1; j >= 0; j--)
+                    if (k < from || j <= at) state = fma0(word_P(w[j]), state, word_Q(w[j]));
+                m.state[x] = state;
+            }
+            __syncthreads();
+        }
+        return;
     }
-    // the tiles behind this window: their words are there, as pairs or already as states
-    for (int j = found + 1; j < i; j += WINDOW) {
-        unsigned long long w[WINDOW];
-#pragma unroll
-        for (int k = 0; k < WINDOW; k++) w[k] = j + k < i ? peek(words + (long long)(j + k) * WIDTH) : 0;
-#pragma unroll
-        for (int k = 0; k < WINDOW; k++)
-            if (j + k < i) state = fma0(word_P(w[k]), state, word_Q(w[k]));
-    }
-    return state;
 }
 
 // Where the block's tile lies.  Tiles are numbered chunk by chunk over all batch entries and
@@ -183,13 +218,7 @@ struct Place {
     int i, strip;        // chunk in walking order
     long long b, tile;   // tile: the strip's first word
 };
-__device__ __forceinline__ Place place_of(const Args &p, unsigned *shared_ticket) {
-    unsigned ticket = blockIdx.x;
-    if (p.counter) {
-        if (threadIdx.x == 0) *shared_ticket = atomicAdd(p.counter, 1u) + 1u;   // the counter starts at all ones
-        __syncthreads();
-        ticket = *shared_ticket;
-    }
+__device__ __forceinline__ Place place_of(const Args &p, unsigned ticket) {
     const unsigned per = (unsigned)(p.a.B * p.strips), i = ticket / per, rest = ticket - i * per;
     Place t;
     t.i = (int)i;
@@ -198,7 +227,6 @@ __device__ __forceinline__ Place place_of(const Args &p, unsigned *shared_ticket
     t.tile = (t.b * p.strips + t.strip) * p.nchunk;
     return t;
 }
-
 // Packed rows: the sequence that starts at, and that ends with, each row of the tile (or -1),
 // and the rows that lie in sequences at all.
 struct Marks {
@@ -206,6 +234,7 @@ struct Marks {
 };
 __device__ __forceinline__ void mark_sequences(const Args &p, Marks &m, long long t0, long long &lo, long long &hi) {
     const int *cu = p.a.cu_seqlens;
+    __syncthreads();   // the last tile's marks have been read
     for (int i = threadIdx.x; i < CHUNK; i += blockDim.x) m.first[i] = m.last[i] = -1;
     __syncthreads();
     for (long long n = threadIdx.x; n < p.nseq; n += blockDim.x) {
@@ -233,352 +262,683 @@ __global__ void pass_all(const float *from, float *to, long long n) {
     if (i < n) to[i] = from ? from[i] : 0.0f;
 }
 
-template <typename TV, typename TG, int FORM, bool HEAD, int V>
-__global__ void __launch_bounds__(Tile<V>::THREADS, 2) scan_forward(Args p) {
-    using S = Tile<V>;
-    __shared__ float sP[S::GROUPS][S::WIDTH], sQ[S::GROUPS][S::WIDTH], sState[S::WIDTH];
-    __shared__ Marks marks;
-    __shared__ unsigned ticket;
-    const Place at = place_of(p, &ticket);
-    const int lane = threadIdx.x % S::LANES, group = threadIdx.x / S::LANES;
-    const int c0 = at.strip * S::WIDTH, c = c0 + lane * V;
-    const bool mine = c < p.C;
-    const bool packed = p.a.cu_seqlens != nullptr;
-    const long long tile0 = (long long)at.i * CHUNK, t0 = tile0 + group * S::ROWS;
-    long long lo = 0, hi = p.a.L;
+// The tensors' maps for the tensor copies: boxes of CHUNK rows by WIDTH channels.
+struct Maps {
+    CUtensorMap g, v, y, dy, dg, dv;
+};
 
-    constexpr int GV = HEAD ? 1 : V;
-    const int gc = HEAD ? c / p.D : c;
-    float k[S::ROWS][GV];
-    Pack<TV, V> v[S::ROWS];
-    {
-        Pack<TG, GV> g[S::ROWS];
-#pragma unroll
-        for (int r = 0; r < S::ROWS; r++) {
-            const bool in = mine && t0 + r < p.a.L;
-            if (in) {
-                g[r] = load<TG, GV>(row<TG>(p.a.g, at.b, t0 + r) + gc);
-                v[r] = load<TV, V>(row<TV>(p.a.v, at.b, t0 + r) + c);
-            }
-        }
-        if (packed) mark_sequences(p, marks, tile0, lo, hi);
-#pragma unroll
-        for (int r = 0; r < S::ROWS; r++) {
-            const bool in = mine && t0 + r >= lo && t0 + r < hi;
-#pragma unroll
-            for (int j = 0; j < GV; j++) k[r][j] = in ? pack_gate<FORM>(to_f(g[r].v[j])) : HOLD<FORM>;
-            if (!in)
-#pragma unroll
-                for (int j = 0; j < V; j++) v[r].v[j] = from_f<TV>(0.0f);
+// A tile of each input tensor in shared memory, two tiles in turn: one tensor copy brings the next
+// tile's while this one is worked on.  Where a thread has read its gates (and values) the products
+// of its gates are kept, and at the end the rows of y, which one tensor copy takes out.  Rows that
+// cannot be copied so (V = 1) go through registers.
+template <typename TV, typename TG, bool HEAD, int V> struct Stage {
+    using S = Tile<TV, V>;
+    static constexpr bool ON = V == 4;
+    static constexpr int G_ROW = S::WIDTH * (int)sizeof(TG), V_ROW = S::WIDTH * (int)sizeof(TV);
+    static constexpr int G_BYTES = HEAD ? 0 : CHUNK * G_ROW, V_BYTES = CHUNK * V_ROW;
+    static constexpr int INPUT_BYTES = ON ? G_BYTES + V_BYTES : 0;
+    __device__ static int at_g(int r) { return (threadIdx.x / S::LANES * S::ROWS + r) * G_ROW + threadIdx.x % S::LANES * 4 * (int)sizeof(TG); }
+    __device__ static int at_v(int r) { return (threadIdx.x / S::LANES * S::ROWS + r) * V_ROW + threadIdx.x % S::LANES * 4 * (int)sizeof(TV); }
+    // four floats where a row's gates were (two-byte gates leave half of the room, the values the rest)
+    __device__ static void keep(char *g, char *v, int r, const float *f) {
+        if constexpr (sizeof(TG) == 4) {
+            *reinterpret_cast<float4 *>(g + at_g(r)) = make_float4(f[0], f[1], f[2], f[3]);
+        } else {
+            *reinterpret_cast<float2 *>(g + at_g(r)) = make_float2(f[0], f[1]);
+            *reinterpret_cast<float2 *>(v + at_v(r)) = make_float2(f[2], f[3]);
         }
     }
-
-    float P[V], Q[V];
-#pragma unroll
-    for (int j = 0; j < V; j++) P[j] = 1.0f, Q[j] = 0.0f;
-#pragma unroll
-    for (int r = 0; r < S::ROWS; r++) {
-        if (packed && mine) {
-            const int n = marks.first[group * S::ROWS + r];
-            if (n >= 0)
-#pragma unroll
-                for (int j = 0; j < V; j++) P[j] = 0.0f, Q[j] = p.a.h0 ? p.a.h0[(long long)n * p.C + c + j] : 0.0f;
+    __device__ static void kept(const char *g, const char *v, int r, float *f) {
+        if constexpr (sizeof(TG) == 4) {
+            const float4 k = *reinterpret_cast<const float4 *>(g + at_g(r));
+            f[0] = k.x, f[1] = k.y, f[2] = k.z, f[3] = k.w;
+        } else {
+            const float2 a = *reinterpret_cast<const float2 *>(g + at_g(r)), b = *reinterpret_cast<const float2 *>(v + at_v(r));
+            f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
         }
+    }
+};
+
+using spectre::tc::fence_proxy_async;
+using spectre::tc::mbar_arrive_expect_tx;
+using spectre::tc::mbar_init;
+using spectre::tc::mbar_wait;
+using spectre::tc::smem_u32;
+
+constexpr uint32_t COPY_POLLS = 4;   // of a millisecond's suspension and more each
+
+__device__ __forceinline__ void tensor_in(char *to, const CUtensorMap *map, int c, int t, int b, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(to)),
+                 "l"(map), "r"(c), "r"(t), "r"(b), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void tensor_out(const CUtensorMap *map, int c, int t, int b, const char *from) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(c), "r"(t), "r"(b),
+                 "r"(smem_u32(from))
+                 : "memory");
+}
+__device__ __forceinline__ void out_close() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void out_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void out_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// A thread's rows of a tile: where they are, and which of them exist.
+template <typename TV, typename TG, bool HEAD, int V> struct Rows {
+    using S = Tile<TV, V>;
+    Place at;
+    int chunk, c0, c, gc;
+    bool mine;
+    long long t0;
+    int count;   // rows before the tensor's end, 0 to ROWS
+    __device__ Rows(const Args &p, unsigned ticket, bool backward) {
+        at = place_of(p, ticket);
+        chunk = backward ? p.nchunk - 1 - at.i : at.i;
+        c0 = at.strip * S::WIDTH;
+        c = c0 + threadIdx.x % S::LANES * V;
+        mine = c < p.C;
+        gc = HEAD ? c / p.D : c;
+        t0 = (long long)chunk * CHUNK + threadIdx.x / S::LANES * S::ROWS;
+        const long long left = p.a.L - t0;
+        count = mine ? (int)(left < 0 ? 0 : left < S::ROWS ? left : S::ROWS) : 0;
+    }
+    template <typename T> __device__ T *first(const gated_scan_rows &r, int column) const { return row<T>(r, at.b, t0) + column; }
+};
+
+constexpr int FORWARD_BLOCKS = 2;   // of 256 threads an SM
+
+template <typename TV, typename TG, int FORM, bool HEAD, int V>
+__global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / Tile<TV, V>::THREADS)
+    scan_forward(const __grid_constant__ Args p, const __grid_constant__ Maps maps) {
+    using S = Tile<TV, V>;
+    using M = Stage<TV, TG, HEAD, V>;
+    using R = Rows<TV, TG, HEAD, V>;
+    constexpr int GV = HEAD ? 1 : V;
+    constexpr bool FAST = sizeof(TV) == 2;
+    constexpr bool KEPT = M::ON && !HEAD;   // the gates' products are in shared memory, not in registers
+    extern __shared__ __align__(128) char buffers[];
+    __shared__ float sP[S::GROUPS][S::WIDTH], sQ[S::GROUPS][S::WIDTH];
+    __shared__ LookBack<S::WIDTH, S::THREADS / S::WIDTH> ahead;
+    __shared__ Marks marks;
+    __shared__ __align__(8) unsigned long long bars[2];
+    const bool packed = p.a.cu_seqlens != nullptr;
+    const int lane = threadIdx.x % S::LANES, group = threadIdx.x / S::LANES;
+    const unsigned tiles = (unsigned)(p.a.B * p.strips) * p.nchunk;
+    // more tiles of a strip in flight than one thread's REACH: ask far at once
+    const bool far = (unsigned)(p.a.B * p.strips) * REACH < gridDim.x;
+
+    const bool agent = threadIdx.x == S::THREADS - 32;   // issues all copies
+    auto fetch = [&](unsigned ticket, int turn) {
+        if (!M::ON || !agent || ticket >= tiles) return;
+        const Place at = place_of(p, ticket);
+        char *to = buffers + turn * M::INPUT_BYTES;
+        const uint32_t bar = smem_u32(&bars[turn]);
+        mbar_arrive_expect_tx(bar, M::INPUT_BYTES);
+        if (!HEAD) tensor_in(to, &maps.g, at.strip * S::WIDTH, at.i * CHUNK, (int)at.b, bar);
+        tensor_in(to + M::G_BYTES, &maps.v, at.strip * S::WIDTH, at.i * CHUNK, (int)at.b, bar);
+    };
+    // one gate a row is too little for a copy: it waits in a register
+    TG g_now[HEAD ? S::ROWS : 1];
+    auto fetch_gates = [&](unsigned ticket) {
+        if (!HEAD || !M::ON || ticket >= tiles) return;
+        const R rows(p, ticket, false);
+        const TG *g = rows.template first<TG>(p.a.g, rows.gc);
+#pragma unroll
+        for (int r = 0; r < (HEAD ? S::ROWS : 1); r++)
+            if (r < rows.count) g_now[r] = g[r * p.a.g.row_stride];
+    };
+    if (M::ON) {
+        if (threadIdx.x == 0) {
+            mbar_init(smem_u32(&bars[0]), 1);
+            mbar_init(smem_u32(&bars[1]), 1);
+        }
+        __syncthreads();
+        fetch(blockIdx.x, 0);
+        fetch_gates(blockIdx.x);
+    }
+    int turn = 0;
+    uint32_t phase = 0;
+    for (unsigned ticket = blockIdx.x; ticket < tiles; ticket += gridDim.x) {
+        char *const pg = buffers + turn * M::INPUT_BYTES, *const pv = pg + M::G_BYTES;
+        const R rows(p, ticket, false);
+        const Place &at = rows.at;
+        const int c0 = rows.c0, c = rows.c;
+        long long lo = 0, hi = p.a.L;
+        bool starts = false, ends = at.i == p.nchunk - 1;   // of sequences in this tile
+        if (packed) {
+            mark_sequences(p, marks, (long long)at.i * CHUNK, lo, hi);
+            bool f = false, l = false;
+            for (int i = threadIdx.x; i < CHUNK; i += S::THREADS) f |= marks.first[i] >= 0, l |= marks.last[i] >= 0;
+            starts = __syncthreads_or(f);
+            ends = __syncthreads_or(l);
+        }
+        const bool all_in = rows.t0 >= lo && rows.t0 + S::ROWS <= hi;
+
+        // row r's state is P[r] h + Q[r], h the state ahead of the thread's rows
+        float P[KEPT ? 1 : S::ROWS][GV], Q[S::ROWS][V], lastP[GV];
+        auto walk = [&](auto careful) {
+            constexpr bool CARE = decltype(careful)::value;   // rows that are missing, starts, factors of zero
+            float q[V];
+#pragma unroll
+            for (int j = 0; j < GV; j++) lastP[j] = 1.0f;
+#pragma unroll
+            for (int j = 0; j < V; j++) q[j] = 0.0f;
+            const TG *gp = rows.template first<TG>(p.a.g, rows.gc);
+            const TV *vp = rows.template first<TV>(p.a.v, c);
+            // all rows first: what is kept goes where they stand.  A careful walk may be a second
+            // one and reads them from memory again.
+            Pack<TG, GV> gs[S::ROWS];
+            Pack<TV, V> vs[S::ROWS];
+#pragma unroll
+            for (int r = 0; r < S::ROWS; r++) {
+                if constexpr (!CARE && M::ON) {
+                    if constexpr (HEAD) gs[r].v[0] = g_now[r];
+                    else gs[r] = load<TG, GV>(reinterpret_cast<const TG *>(pg + M::at_g(r)));
+                    vs[r] = load<TV, V>(reinterpret_cast<const TV *>(pv + M::at_v(r)));
+                } else if (r < rows.count) {
+                    gs[r] = load<TG, GV>(gp + r * p.a.g.row_stride);
+                    vs[r] = load<TV, V>(vp + r * p.a.v.row_stride);
+                }
+            }
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int r = 0; r < S::ROWS; r++) {
+                if (CARE && starts) {
+                    const int n = rows.mine ? marks.first[group * S::ROWS + r] : -1;
+                    if (n >= 0) {
+#pragma unroll
+                        for (int j = 0; j < GV; j++) lastP[j] = 0.0f;
+#pragma unroll
+                        for (int j = 0; j < V; j++) q[j] = p.a.h0 ? p.a.h0[(long long)n * p.C + c + j] : 0.0f;
+                    }
+                }
+                if (!CARE || (r < rows.count && rows.t0 + r >= lo && rows.t0 + r < hi)) {
+                    const Pack<TG, GV> &g = gs[r];
+                    const Pack<TV, V> &v = vs[r];
+                    Gate k[GV];
+#pragma unroll
+                    for (int j = 0; j < GV; j++) {
+                        k[j] = gate_of<FORM, FAST>(to_f(g.v[j]));
+                        lastP[j] *= k[j].a;
+                    }
+#pragma unroll
+                    for (int j = 0; j < V; j++) {
+                        const Gate &kj = k[HEAD ? 0 : j];
+                        const float vj = to_f(v.v[j]);
+                        q[j] = fma_if<CARE>(kj.a, q[j], FORM == GATED_SCAN_EXP ? vj : mul_if<CARE>(kj.c, vj));
+                    }
+                }
+                if constexpr (KEPT)
+                    M::keep(pg, pv, r, lastP);
+                else
+#pragma unroll
+                    for (int j = 0; j < GV; j++) P[r][j] = lastP[j];
+#pragma unroll
+                for (int j = 0; j < V; j++) Q[r][j] = q[j];
+            }
+        };
+        bool arrived = true;
+        if (M::ON) arrived = mbar_wait(smem_u32(&bars[turn]), phase, COPY_POLLS * 1000);
+        // Without care a NaN or infinity anywhere leaves the last row without a finite value: then
+        // the rows are walked again.
+        bool fine = rows.count == S::ROWS && all_in && !starts && arrived;
+        if (fine) {
+            walk(std::false_type{});
+#pragma unroll
+            for (int j = 0; j < V; j++) fine &= finite(Q[S::ROWS - 1][j]);
+        }
+        if (!fine) walk(std::true_type{});
 #pragma unroll
         for (int j = 0; j < V; j++) {
-            const Gate q = open_gate<FORM>(k[r][HEAD ? 0 : j]);
-            Q[j] = fma0(q.a, Q[j], input_of<FORM>(q, to_f(v[r].v[j])));
-            P[j] *= q.a;
+            sP[group][lane * V + j] = lastP[HEAD ? 0 : j];
+            sQ[group][lane * V + j] = arrived ? Q[S::ROWS - 1][j] : __uint_as_float(0x7fc00000u);
         }
-    }
-#pragma unroll
-    for (int j = 0; j < V; j++) sP[group][lane * V + j] = P[j], sQ[group][lane * V + j] = Q[j];
-    __syncthreads();
+        __syncthreads();
 
-    if (threadIdx.x < S::WIDTH) {
-        // each group's pair becomes that of all groups ahead of it
-        const int x = threadIdx.x, cx = c0 + x;
+        if (M::ON && agent) out_read();   // the other buffer's rows of y have left it
+        fetch(ticket + gridDim.x, turn ^ 1);
+        fetch_gates(ticket + gridDim.x);
+        const int x = threadIdx.x, cx = c0 + threadIdx.x % S::WIDTH;
+        unsigned long long *const words = p.words + at.tile * S::WIDTH;
+        const bool more = at.i + 1 < p.nchunk;
         float allP = 1.0f, allQ = 0.0f;
+        if (x < S::WIDTH) {
+            // each group's pair becomes that of all groups ahead of it
 #pragma unroll
-        for (int i = 0; i < S::GROUPS; i++) {
-            const float gP = sP[i][x], gQ = sQ[i][x];
-            sP[i][x] = allP;
-            sQ[i][x] = allQ;
-            allQ = fma0(gP, allQ, gQ);
-            allP *= gP;
-        }
-        float state = 0.0f;
-        if (cx < p.C) {
-            unsigned long long *words = p.words + at.tile * S::WIDTH + x;
-            const bool more = at.i + 1 < p.nchunk;
-            if (at.i == 0) {
-                if (!packed && p.a.h0) state = p.a.h0[at.b * p.C + cx];
-            } else {
-                if (more && allP != 0.0f) publish(words + (long long)at.i * S::WIDTH, allP, allQ);
-                state = look_back<S::WIDTH>(words, at.i);
+            for (int i = 0; i < S::GROUPS; i++) {
+                const float gP = sP[i][x], gQ = sQ[i][x];
+                sP[i][x] = allP;
+                sQ[i][x] = allQ;
+                allQ = fma0(gP, allQ, gQ);
+                allP *= gP;
             }
-            if (more) publish(words + (long long)at.i * S::WIDTH, 0.0f, fma0(allP, state, allQ));
+            if (at.i > 0 && more && cx < p.C && allP != 0.0f) publish(words + (long long)at.i * S::WIDTH + x, allP, allQ);
+        }
+        if (at.i > 0) {
+            look_back(ahead, words, at.i, cx < p.C, far);
+        } else {
+            if (x < S::WIDTH) ahead.state[x] = !packed && p.a.h0 && cx < p.C ? p.a.h0[at.b * p.C + cx] : 0.0f;
+            __syncthreads();
+        }
+        if (x < S::WIDTH && cx < p.C) {
+            const float state = ahead.state[x];
+            if (more) publish(words + (long long)at.i * S::WIDTH + x, 0.0f, fma0(allP, state, allQ));
             if (p.a.states) p.a.states[(at.b * p.nchunk + at.i) * p.C + cx] = state;
         }
-        sState[x] = state;
-    }
-    __syncthreads();
 
-    if (mine) {
-        float h[V];
+        float h0[V];
+        fine = true;
 #pragma unroll
-        for (int j = 0; j < V; j++) h[j] = fma0(sP[group][lane * V + j], sState[lane * V + j], sQ[group][lane * V + j]);
+        for (int j = 0; j < V; j++) {
+            h0[j] = fma0(sP[group][lane * V + j], ahead.state[lane * V + j], sQ[group][lane * V + j]);
+            fine &= finite(h0[j]);
+        }
+        const long long tile0 = (long long)at.i * CHUNK;
+        const bool whole = !packed || (tile0 >= lo && tile0 + CHUNK <= hi);   // the tile's rows are all written, or do not exist
+        TV *y = rows.template first<TV>(p.a.y, c);
 #pragma unroll
         for (int r = 0; r < S::ROWS; r++) {
-            const long long t = t0 + r;
-            if (t >= p.a.L) break;
-            if (packed) {
-                const int n = marks.first[group * S::ROWS + r];
+            if (r >= rows.count) break;
+            float h[V], pr[M::ON && !HEAD ? 4 : GV];
+            if constexpr (KEPT) {
+                M::kept(pg, pv, r, pr);
+            } else {
+#pragma unroll
+                for (int j = 0; j < GV; j++) pr[j] = P[r][j];
+            }
+#pragma unroll
+            for (int j = 0; j < V; j++) h[j] = fmaf(pr[HEAD ? 0 : j], h0[j], Q[r][j]);
+            if (!fine)
+#pragma unroll
+                for (int j = 0; j < V; j++) h[j] = fma0(pr[HEAD ? 0 : j], h0[j], Q[r][j]);
+            const bool in = all_in || (rows.t0 + r >= lo && rows.t0 + r < hi);
+            if (ends && in && p.a.hT) {
+                const long long n = packed ? marks.last[group * S::ROWS + r] : rows.t0 + r == p.a.L - 1 ? at.b : -1;
                 if (n >= 0)
 #pragma unroll
-                    for (int j = 0; j < V; j++) h[j] = p.a.h0 ? p.a.h0[(long long)n * p.C + c + j] : 0.0f;
+                    for (int j = 0; j < V; j++) p.a.hT[n * p.C + c + j] = h[j];
             }
+            if (M::ON && whole) {
+                store<TV, V>(reinterpret_cast<TV *>(pv + M::at_v(r)), h);
+                continue;
+            }
+            if (!in) {
+                if (!p.a.zero_outside) continue;
 #pragma unroll
-            for (int j = 0; j < V; j++) {
-                const Gate q = open_gate<FORM>(k[r][HEAD ? 0 : j]);
-                h[j] = fma0(q.a, h[j], input_of<FORM>(q, to_f(v[r].v[j])));
+                for (int j = 0; j < V; j++) h[j] = 0.0f;
             }
-            if (t >= lo && t < hi) {
-                store<TV, V>(row<TV>(p.a.y, at.b, t) + c, h);
-                if (p.a.hT) {
-                    const long long n = packed ? marks.last[group * S::ROWS + r] : t == p.a.L - 1 ? at.b : -1;
-                    if (n >= 0)
-#pragma unroll
-                        for (int j = 0; j < V; j++) p.a.hT[n * p.C + c + j] = h[j];
-                }
-            } else if (p.a.zero_outside) {
-                const float zero[V] = {};
-                store<TV, V>(row<TV>(p.a.y, at.b, t) + c, zero);
+            store<TV, V>(y + r * p.a.y.row_stride, h);
+        }
+        if (packed && at.i == 0) pass_empty(p, p.a.h0, p.a.hT, c0, S::WIDTH);
+        if (M::ON) {
+            fence_proxy_async();
+            __syncthreads();
+            if (agent && whole) {
+                tensor_out(&maps.y, c0, at.i * CHUNK, (int)at.b, pv);
+                out_close();
             }
+            phase ^= turn;
+            turn ^= 1;
         }
     }
-    if (packed && at.i == 0) pass_empty(p, p.a.h0, p.a.hT, c0, S::WIDTH);
+    if (M::ON && agent) out_done();
 }
 
 // The strips that the channels of head h lie in.
 __host__ __device__ __forceinline__ int first_strip(int h, int D, int width) { return (int)((long long)h * D / width); }
 __host__ __device__ __forceinline__ int last_strip(int h, int D, int width) { return (int)(((long long)h * D + D - 1) / width); }
 
+constexpr int BACKWARD_BLOCKS = 2;   // an SM: 128 registers a thread, 111 KB of shared memory
+
 template <typename TV, typename TG, int FORM, bool HEAD, int V>
-__global__ void __launch_bounds__(Tile<V>::THREADS, 2) scan_backward(Args p) {
-    using S = Tile<V>;
-    // (P, Q) of the states going forward, (R, E) of the gradients going back
-    __shared__ float sP[S::GROUPS][S::WIDTH], sQ[S::GROUPS][S::WIDTH];
-    __shared__ float sR[S::GROUPS][S::WIDTH], sE[S::GROUPS][S::WIDTH], sGrad[S::WIDTH];
-    __shared__ Marks marks;
-    __shared__ unsigned ticket;
-    const Place at = place_of(p, &ticket);
-    const int chunk = p.nchunk - 1 - at.i;
-    const int lane = threadIdx.x % S::LANES, group = threadIdx.x / S::LANES;
-    const int c0 = at.strip * S::WIDTH, c = c0 + lane * V;
-    const bool mine = c < p.C;
-    const bool packed = p.a.cu_seqlens != nullptr;
-    const long long tile0 = (long long)chunk * CHUNK, t0 = tile0 + group * S::ROWS;
-    long long lo = 0, hi = p.a.L;
-
+__global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
+    scan_backward(const __grid_constant__ Args p, const __grid_constant__ Maps maps) {
+    using S = Tile<TV, V>;
+    using M = Stage<TV, TG, HEAD, V>;
+    using R = Rows<TV, TG, HEAD, V>;
     constexpr int GV = HEAD ? 1 : V;
-    const int gc = HEAD ? c / p.D : c;
-    float k[S::ROWS][GV];
-    Pack<TV, V> v[S::ROWS], dy[S::ROWS];
-    {
-        Pack<TG, GV> g[S::ROWS];
+    constexpr bool FAST = sizeof(TV) == 2;
+    constexpr int TILE_BYTES = M::ON ? M::INPUT_BYTES + M::V_BYTES : 0;   // g, v, dy
+    constexpr bool IN_PLACE = M::ON && !HEAD;   // the groups' P stand where their gates were
+    extern __shared__ __align__(128) char buffers[];
+    // (P, Q) of the states going forward, (R, E) of the gradients going back
+    __shared__ float sP[IN_PLACE ? 1 : S::GROUPS][S::WIDTH], sQ[S::GROUPS][S::WIDTH];
+    __shared__ float sR[S::GROUPS][S::WIDTH], sE[S::GROUPS][S::WIDTH];
+    __shared__ LookBack<S::WIDTH, S::THREADS / S::WIDTH> ahead;
+    __shared__ Marks marks;
+    __shared__ __align__(8) unsigned long long bars[2];
+    const bool packed = p.a.cu_seqlens != nullptr;
+    const int lane = threadIdx.x % S::LANES, group = threadIdx.x / S::LANES;
+    const unsigned tiles = (unsigned)(p.a.B * p.strips) * p.nchunk;
+    const bool far = (unsigned)(p.a.B * p.strips) * REACH < gridDim.x;
+
+    const bool agent = threadIdx.x == S::THREADS - 32;   // issues all copies
+    auto fetch = [&](unsigned ticket, int turn) {
+        if (!M::ON || !agent || ticket >= tiles) return;
+        const Place at = place_of(p, ticket);
+        char *to = buffers + turn * TILE_BYTES;
+        const uint32_t bar = smem_u32(&bars[turn]);
+        const int c0 = at.strip * S::WIDTH, t0 = (p.nchunk - 1 - at.i) * CHUNK;
+        mbar_arrive_expect_tx(bar, TILE_BYTES);
+        if (!HEAD) tensor_in(to, &maps.g, c0, t0, (int)at.b, bar);
+        tensor_in(to + M::G_BYTES, &maps.v, c0, t0, (int)at.b, bar);
+        tensor_in(to + M::INPUT_BYTES, &maps.dy, c0, t0, (int)at.b, bar);
+    };
+    TG g_now[HEAD ? S::ROWS : 1];
+    auto fetch_gates = [&](unsigned ticket) {
+        if (!HEAD || !M::ON || ticket >= tiles) return;
+        const R rows(p, ticket, true);
+        const TG *g = rows.template first<TG>(p.a.g, rows.gc);
 #pragma unroll
-        for (int r = 0; r < S::ROWS; r++) {
-            if (mine && t0 + r < p.a.L) {
-                g[r] = load<TG, GV>(row<TG>(p.a.g, at.b, t0 + r) + gc);
-                v[r] = load<TV, V>(row<TV>(p.a.v, at.b, t0 + r) + c);
-                dy[r] = load<TV, V>(row<TV>(p.a.dy, at.b, t0 + r) + c);
+        for (int r = 0; r < (HEAD ? S::ROWS : 1); r++)
+            if (r < rows.count) g_now[r] = g[r * p.a.g.row_stride];
+    };
+    if (M::ON) {
+        if (threadIdx.x == 0) {
+            mbar_init(smem_u32(&bars[0]), 1);
+            mbar_init(smem_u32(&bars[1]), 1);
+        }
+        __syncthreads();
+        fetch(blockIdx.x, 0);
+        fetch_gates(blockIdx.x);
+    }
+    int turn = 0;
+    uint32_t phase = 0;
+    for (unsigned ticket = blockIdx.x; ticket < tiles; ticket += gridDim.x) {
+        char *const pg = buffers + turn * TILE_BYTES, *const pv = pg + M::G_BYTES, *const pd = pg + M::INPUT_BYTES;
+        const R rows(p, ticket, true);
+        const Place &at = rows.at;
+        const int c0 = rows.c0, c = rows.c;
+        const long long tile0 = (long long)rows.chunk * CHUNK;
+        long long lo = 0, hi = p.a.L;
+        bool edges = rows.chunk == 0 || at.i == 0;   // a sequence starts or ends in this tile
+        if (packed) {
+            mark_sequences(p, marks, tile0, lo, hi);
+            bool f = false;
+            for (int i = threadIdx.x; i < CHUNK; i += S::THREADS) f |= marks.first[i] >= 0 || marks.last[i] >= 0;
+            edges = __syncthreads_or(f);
+        }
+        const bool all_in = rows.t0 >= lo && rows.t0 + S::ROWS <= hi;
+        auto in = [&](int r) { return r < rows.count && rows.t0 + r >= lo && rows.t0 + r < hi; };
+        // the sequence that row r starts or ends, or -1
+        auto starts = [&](int r) -> long long {
+            if (!rows.mine) return -1;
+            if (packed) return marks.first[group * S::ROWS + r];
+            return rows.t0 + r == 0 ? at.b : -1;
+        };
+        auto ends = [&](int r) -> long long {
+            if (!rows.mine) return -1;
+            if (packed) return marks.last[group * S::ROWS + r];
+            return rows.t0 + r == p.a.L - 1 ? at.b : -1;
+        };
+
+        bool arrived = true;
+        if (M::ON) arrived = mbar_wait(smem_u32(&bars[turn]), phase, COPY_POLLS * 1000);
+        // the rows' gates stay in registers, values and dy where the copies put them (V = 1: in registers)
+        float k[S::ROWS][GV];
+        Pack<TV, V> own_v[M::ON ? 1 : S::ROWS], own_d[M::ON ? 1 : S::ROWS];
+        {
+            const TG *gp = rows.template first<TG>(p.a.g, rows.gc);
+            const TV *vp = rows.template first<TV>(p.a.v, c), *dp = rows.template first<TV>(p.a.dy, c);
+#pragma unroll
+            for (int r = 0; r < S::ROWS; r++) {
+                Pack<TG, GV> g;
+                const bool there = in(r);
+                if constexpr (M::ON) {
+                    if constexpr (HEAD) g.v[0] = g_now[r];
+                    else g = load<TG, GV>(reinterpret_cast<const TG *>(pg + M::at_g(r)));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V; j++) own_v[r].v[j] = own_d[r].v[j] = from_f<TV>(0.0f);
+                    if (there) {
+                        g = load<TG, GV>(gp + r * p.a.g.row_stride);
+                        own_v[r] = load<TV, V>(vp + r * p.a.v.row_stride);
+                        own_d[r] = load<TV, V>(dp + r * p.a.dy.row_stride);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < GV; j++) k[r][j] = there ? pack_gate<FORM, FAST>(to_f(g.v[j])) : HOLD<FORM>;
             }
         }
-        if (packed) mark_sequences(p, marks, tile0, lo, hi);
+        // row r of values or dy; rows that are missing or in no sequence are zero
+        auto value = [&](auto careful, int r, float *f) {
+            Pack<TV, V> x;
+            if constexpr (M::ON) x = load<TV, V>(reinterpret_cast<const TV *>(pv + M::at_v(r)));
+            else x = own_v[r];
 #pragma unroll
-        for (int r = 0; r < S::ROWS; r++) {
-            const bool in = mine && t0 + r >= lo && t0 + r < hi;
+            for (int j = 0; j < V; j++) f[j] = !decltype(careful)::value || in(r) ? to_f(x.v[j]) : 0.0f;
+        };
+        auto gradient = [&](auto careful, int r, float *f) {
+            Pack<TV, V> x;
+            if constexpr (M::ON) x = load<TV, V>(reinterpret_cast<const TV *>(pd + M::at_v(r)));
+            else x = own_d[r];
 #pragma unroll
-            for (int j = 0; j < GV; j++) k[r][j] = in ? pack_gate<FORM>(to_f(g[r].v[j])) : HOLD<FORM>;
-            if (!in)
-#pragma unroll
-                for (int j = 0; j < V; j++) v[r].v[j] = dy[r].v[j] = from_f<TV>(0.0f);
-        }
-    }
+            for (int j = 0; j < V; j++) f[j] = !decltype(careful)::value || in(r) ? to_f(x.v[j]) : 0.0f;
+        };
 
-    // the sequence that row r starts or ends, or -1
-    auto starts = [&](int r) -> long long {
-        if (packed) return marks.first[group * S::ROWS + r];
-        return t0 + r == 0 ? at.b : -1;
-    };
-    auto ends = [&](int r) -> long long {
-        if (packed) return marks.last[group * S::ROWS + r];
-        return t0 + r == p.a.L - 1 ? at.b : -1;
-    };
-
-    float P[V], Q[V];
+        float P[V], Q[V], T[V], E[V];
+        auto walk = [&](auto careful) {
+            constexpr bool CARE = decltype(careful)::value;
 #pragma unroll
-    for (int j = 0; j < V; j++) P[j] = 1.0f, Q[j] = 0.0f;
+            for (int j = 0; j < V; j++) P[j] = T[j] = 1.0f, Q[j] = E[j] = 0.0f;
 #pragma unroll
-    for (int r = 0; r < S::ROWS; r++) {
-        const long long n = packed && mine ? starts(r) : -1;
-        if (n >= 0)
+            for (int r = 0; r < S::ROWS; r++) {
+                if (CARE && packed && edges) {
+                    const long long n = starts(r);
+                    if (n >= 0)
 #pragma unroll
-            for (int j = 0; j < V; j++) P[j] = 0.0f, Q[j] = p.a.h0 ? p.a.h0[n * p.C + c + j] : 0.0f;
+                        for (int j = 0; j < V; j++) P[j] = 0.0f, Q[j] = p.a.h0 ? p.a.h0[n * p.C + c + j] : 0.0f;
+                }
+                float v[V];
+                value(careful, r, v);
 #pragma unroll
-        for (int j = 0; j < V; j++) {
-            const Gate q = open_gate<FORM>(k[r][HEAD ? 0 : j]);
-            Q[j] = fma0(q.a, Q[j], input_of<FORM>(q, to_f(v[r].v[j])));
-            P[j] *= q.a;
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < V; j++) sP[group][lane * V + j] = P[j], sQ[group][lane * V + j] = Q[j];
-#pragma unroll
-    for (int j = 0; j < V; j++) P[j] = 1.0f, Q[j] = 0.0f;
-#pragma unroll
-    for (int r = S::ROWS - 1; r >= 0; r--) {
-        const long long n = mine ? ends(r) : -1;
-        if (n >= 0)
-#pragma unroll
-            for (int j = 0; j < V; j++) P[j] = 0.0f, Q[j] = p.a.dhT ? p.a.dhT[n * p.C + c + j] : 0.0f;
-#pragma unroll
-        for (int j = 0; j < V; j++) {
-            const Gate q = open_gate<FORM>(k[r][HEAD ? 0 : j]);
-            Q[j] = mul0(q.a, to_f(dy[r].v[j]) + Q[j]);
-            P[j] *= q.a;
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < V; j++) sR[group][lane * V + j] = P[j], sE[group][lane * V + j] = Q[j];
-    __syncthreads();
-
-    // one warp or two join the gradients and look back; others find the groups' states
-    if (threadIdx.x < S::WIDTH) {
-        const int x = threadIdx.x, cx = c0 + x;
-        float allP = 1.0f, allQ = 0.0f;
-#pragma unroll
-        for (int i = S::GROUPS - 1; i >= 0; i--) {
-            const float gP = sR[i][x], gQ = sE[i][x];
-            sR[i][x] = allP;
-            sE[i][x] = allQ;
-            allQ = fma0(gP, allQ, gQ);
-            allP *= gP;
-        }
-        float grad = 0.0f;
-        if (cx < p.C) {
-            unsigned long long *words = p.words + at.tile * S::WIDTH + x;
-            const bool more = at.i + 1 < p.nchunk;
-            if (at.i > 0) {
-                if (more && allP != 0.0f) publish(words + (long long)at.i * S::WIDTH, allP, allQ);
-                grad = look_back<S::WIDTH>(words, at.i);
+                for (int j = 0; j < V; j++) {
+                    const Gate q = open_gate<FORM>(k[r][HEAD ? 0 : j]);
+                    Q[j] = fma_if<CARE>(q.a, Q[j], FORM == GATED_SCAN_EXP ? v[j] : mul_if<CARE>(q.c, v[j]));
+                    P[j] *= q.a;
+                }
             }
-            if (more) publish(words + (long long)at.i * S::WIDTH, 0.0f, fma0(allP, grad, allQ));
+#pragma unroll
+            for (int r = S::ROWS - 1; r >= 0; r--) {
+                if (CARE && edges) {
+                    const long long n = ends(r);
+                    if (n >= 0)
+#pragma unroll
+                        for (int j = 0; j < V; j++) T[j] = 0.0f, E[j] = p.a.dhT ? p.a.dhT[n * p.C + c + j] : 0.0f;
+                }
+                float d[V];
+                gradient(careful, r, d);
+#pragma unroll
+                for (int j = 0; j < V; j++) {
+                    const float a = open_gate<FORM>(k[r][HEAD ? 0 : j]).a;
+                    E[j] = mul_if<CARE>(a, d[j] + E[j]);
+                    T[j] *= a;
+                }
+            }
+        };
+        bool fine = rows.count == S::ROWS && all_in && !edges;
+        if (fine) {
+            walk(std::false_type{});
+#pragma unroll
+            for (int j = 0; j < V; j++) fine &= finite(Q[j]) && finite(E[j]);
         }
-        sGrad[x] = grad;
-    } else if (threadIdx.x < 2 * S::WIDTH) {
-        const int x = threadIdx.x - S::WIDTH, cx = c0 + x;
-        float h = cx < p.C ? p.a.states[(at.b * p.nchunk + chunk) * p.C + cx] : 0.0f;
-#pragma unroll
-        for (int i = 0; i < S::GROUPS; i++) {
-            const float gP = sP[i][x], gQ = sQ[i][x];
-            sQ[i][x] = h;
-            h = fma0(gP, h, gQ);
-        }
-    }
-    __syncthreads();
-
-    // forward again for the gate's slope at every row, then back with the gradient
-    float slope[S::ROWS][V];
-    float h[V], e[V];
-#pragma unroll
-    for (int j = 0; j < V; j++) {
-        h[j] = sQ[group][lane * V + j];
-        e[j] = fma0(sR[group][lane * V + j], sGrad[lane * V + j], sE[group][lane * V + j]);
-    }
-#pragma unroll
-    for (int r = 0; r < S::ROWS; r++) {
-        const long long n = packed && mine ? starts(r) : -1;
-        if (n >= 0)
-#pragma unroll
-            for (int j = 0; j < V; j++) h[j] = p.a.h0 ? p.a.h0[n * p.C + c + j] : 0.0f;
+        if (!fine) walk(std::true_type{});
 #pragma unroll
         for (int j = 0; j < V; j++) {
-            const Gate q = open_gate<FORM>(k[r][HEAD ? 0 : j]);
-            const float vv = to_f(v[r].v[j]);
-            slope[r][j] = slope_of<FORM>(q, h[j], vv);
-            h[j] = fma0(q.a, h[j], input_of<FORM>(q, vv));
+            sQ[group][lane * V + j] = Q[j];
+            sR[group][lane * V + j] = T[j];
+            sE[group][lane * V + j] = arrived ? E[j] : __uint_as_float(0x7fc00000u);
         }
-    }
-    // lanes of one head: lane + o still in it
-    bool same[4];
-    int pieces = 1, piece = 0;
-    bool leader = true;
-    if (HEAD) {
+        if constexpr (IN_PLACE) {
+            // float4 in the first row's gates, or a half in each of the first two
+            float *a = reinterpret_cast<float *>(pg + M::at_g(0)), *b = reinterpret_cast<float *>(pg + M::at_g(1));
+            asm volatile("" ::: "memory");   // the gates have been read
 #pragma unroll
-        for (int o = 0; o < 4; o++) {
-            const int other = c + (V << o);
-            same[o] = lane + (1 << o) < S::LANES && other < p.C && other / p.D == gc;
-        }
-        leader = mine && (lane == 0 || (c - V) / p.D != gc);
-        if (mine) piece = at.strip - first_strip(gc, p.D, S::WIDTH);
-        pieces = p.parts ? 2 : 1;
-    }
-    const bool wide5 = HEAD && S::LANES == 32;
-    const bool same5 = wide5 && lane + 16 < S::LANES && c + 16 * V < p.C && (c + 16 * V) / p.D == gc;
-#pragma unroll
-    for (int r = S::ROWS - 1; r >= 0; r--) {
-        const long long t = t0 + r;
-        const bool in = mine && t >= lo && t < hi;
-        const long long n = mine && t < p.a.L ? ends(r) : -1;
-        if (n >= 0)
-#pragma unroll
-            for (int j = 0; j < V; j++) e[j] = p.a.dhT ? p.a.dhT[n * p.C + c + j] : 0.0f;
-        float dv[V], dg[V];
-#pragma unroll
-        for (int j = 0; j < V; j++) {
-            const Gate q = open_gate<FORM>(k[r][HEAD ? 0 : j]);
-            const float dh = to_f(dy[r].v[j]) + e[j];
-            dg[j] = slope[r][j] * dh;
-            dv[j] = FORM == GATED_SCAN_EXP ? dh : mul0(q.c, dh);
-            e[j] = mul0(q.a, dh);
-        }
-        if (mine && t < p.a.L && !in && p.a.zero_outside)
-#pragma unroll
-            for (int j = 0; j < V; j++) dv[j] = dg[j] = 0.0f;
-        const bool write = in || (mine && t < p.a.L && p.a.zero_outside);
-        if (write) store<TV, V>(row<TV>(p.a.dv, at.b, t) + c, dv);
-        if constexpr (!HEAD) {
-            if (write) store<TG, V>(row<TG>(p.a.dg, at.b, t) + c, dg);
+            for (int j = 0; j < 4; j++) (sizeof(TG) == 4 || j < 2 ? a[j] : b[j - 2]) = P[j];
         } else {
-            float s = 0.0f;
 #pragma unroll
-            for (int j = 0; j < V; j++) s += write ? dg[j] : 0.0f;
+            for (int j = 0; j < V; j++) sP[group][lane * V + j] = P[j];
+        }
+        __syncthreads();
+
+        if (M::ON && agent) out_read();   // the other buffer's gradients have left it
+        fetch(ticket + gridDim.x, turn ^ 1);
+        fetch_gates(ticket + gridDim.x);
+        const int x = threadIdx.x, cx = c0 + threadIdx.x % S::WIDTH;
+        unsigned long long *const words = p.words + at.tile * S::WIDTH;
+        const bool more = at.i + 1 < p.nchunk;
+        float allT = 1.0f, allE = 0.0f;
+        if (x < S::WIDTH) {
+            // each group's pair becomes that of all groups ahead of it, going back
 #pragma unroll
-            for (int o = 0; o < 4; o++) {
-                const float other = __shfl_down_sync(0xffffffffu, s, 1 << o, S::LANES);
-                s += same[o] ? other : 0.0f;
+            for (int i = S::GROUPS - 1; i >= 0; i--) {
+                const float gT = sR[i][x], gE = sE[i][x];
+                sR[i][x] = allT;
+                sE[i][x] = allE;
+                allE = fma0(gT, allE, gE);
+                allT *= gT;
             }
-            if (wide5) {
-                const float other = __shfl_down_sync(0xffffffffu, s, 16, S::LANES);
-                s += same5 ? other : 0.0f;
-            }
-            if (write && leader) {
-                if (pieces == 1)
-                    row<TG>(p.a.dg, at.b, t)[gc] = from_f<TG>(s);
+            if (at.i > 0 && more && cx < p.C && allT != 0.0f) publish(words + (long long)at.i * S::WIDTH + x, allT, allE);
+        } else if (x < 2 * S::WIDTH) {
+            // each group's result becomes the state ahead of it
+            const int y = x - S::WIDTH;
+            float h = cx < p.C ? p.a.states[(at.b * p.nchunk + rows.chunk) * p.C + cx] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < S::GROUPS; i++) {
+                float gP;
+                if constexpr (IN_PLACE)
+                    gP = sizeof(TG) == 4 ? *reinterpret_cast<const float *>(pg + i * S::ROWS * M::G_ROW + y * 4)
+                                         : *reinterpret_cast<const float *>(pg + (i * S::ROWS + y % 4 / 2) * M::G_ROW + y / 4 * 8 + y % 2 * 4);
                 else
-                    p.parts[(piece * p.a.B * p.a.L + at.b * p.a.L + t) * p.H + gc] = s;
+                    gP = sP[i][y];
+                const float gQ = sQ[i][y];
+                sQ[i][y] = h;
+                h = fma0(gP, h, gQ);
             }
         }
-        if (in && p.a.dh0) {
-            const long long m = starts(r);
-            if (m >= 0)
+        if (at.i > 0) {
+            look_back(ahead, words, at.i, cx < p.C, far);
+        } else {
+            if (x < S::WIDTH) ahead.state[x] = 0.0f;
+            __syncthreads();
+        }
+        if (x < S::WIDTH && cx < p.C && more) publish(words + (long long)at.i * S::WIDTH + x, 0.0f, fma0(allT, ahead.state[x], allE));
+
+        const bool whole = !packed || (tile0 >= lo && tile0 + CHUNK <= hi);   // the tile's rows are all written, or do not exist
+        float h[V], e[V];
 #pragma unroll
-                for (int j = 0; j < V; j++) p.a.dh0[m * p.C + c + j] = e[j];
+        for (int j = 0; j < V; j++) {
+            h[j] = sQ[group][lane * V + j];
+            e[j] = fma0(sR[group][lane * V + j], ahead.state[lane * V + j], sE[group][lane * V + j]);
+            fine &= finite(h[j]) && finite(e[j]);
+        }
+        // lanes of one head: lane + 2^o is still in it
+        bool same[5], leader = true;
+        if (HEAD) {
+#pragma unroll
+            for (int o = 0; o < 5; o++) {
+                const int other = c + (V << o);
+                same[o] = lane + (1 << o) < S::LANES && other < p.C && other / p.D == rows.gc;
+            }
+            leader = rows.mine && (lane == 0 || (c - V) / p.D != rows.gc);
+        }
+        const int piece = HEAD && rows.mine ? at.strip - first_strip(rows.gc, p.D, S::WIDTH) : 0;
+        // forward again for the gate's slope at every row, then back with the gradient
+        auto finish = [&](auto careful) {
+            constexpr bool CARE = decltype(careful)::value;
+            float slope[S::ROWS][V];
+#pragma unroll
+            for (int r = 0; r < S::ROWS; r++) {
+                if (CARE && packed && edges) {
+                    const long long n = starts(r);
+                    if (n >= 0)
+#pragma unroll
+                        for (int j = 0; j < V; j++) h[j] = p.a.h0 ? p.a.h0[n * p.C + c + j] : 0.0f;
+                }
+                float v[V];
+                value(careful, r, v);
+#pragma unroll
+                for (int j = 0; j < V; j++) {
+                    const Gate q = open_gate<FORM>(k[r][HEAD ? 0 : j]);
+                    slope[r][j] = FORM == GATED_SCAN_EXP ? mul_if<CARE>(q.a, h[j]) : mul_if<CARE>(q.a * q.c, h[j] - v[j]);
+                    h[j] = fma_if<CARE>(q.a, h[j], FORM == GATED_SCAN_EXP ? v[j] : mul_if<CARE>(q.c, v[j]));
+                }
+            }
+            asm volatile("" ::: "memory");   // dv goes where the values were
+            TV *dv_row = rows.template first<TV>(p.a.dv, c);
+            TG *dg_row = rows.template first<TG>(p.a.dg, rows.gc);
+#pragma unroll
+            for (int r = S::ROWS - 1; r >= 0; r--) {
+                const bool here = !CARE || in(r);
+                if (CARE && edges) {
+                    const long long n = ends(r);
+                    if (n >= 0)
+#pragma unroll
+                        for (int j = 0; j < V; j++) e[j] = p.a.dhT ? p.a.dhT[n * p.C + c + j] : 0.0f;
+                }
+                float d[V], dv[V], dg[V];
+                gradient(careful, r, d);
+#pragma unroll
+                for (int j = 0; j < V; j++) {
+                    const Gate q = open_gate<FORM>(k[r][HEAD ? 0 : j]);
+                    const float dh = d[j] + e[j];
+                    dg[j] = here ? slope[r][j] * dh : 0.0f;
+                    dv[j] = !here ? 0.0f : FORM == GATED_SCAN_EXP ? dh : mul_if<CARE>(q.c, dh);
+                    e[j] = mul_if<CARE>(q.a, dh);
+                }
+                // straight to memory: rows of tiles that are not whole, one by one
+                const bool write = here || (r < rows.count && p.a.zero_outside);
+                if (M::ON && whole)
+                    store<TV, V>(reinterpret_cast<TV *>(pv + M::at_v(r)), dv);
+                else if (write)
+                    store<TV, V>(dv_row + r * p.a.dv.row_stride, dv);
+                if constexpr (!HEAD) {
+                    if (M::ON && whole)
+                        store<TG, V>(reinterpret_cast<TG *>(pg + M::at_g(r)), dg);
+                    else if (write)
+                        store<TG, V>(dg_row + r * p.a.dg.row_stride, dg);
+                } else {
+                    float s = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < V; j++) s += dg[j];
+#pragma unroll
+                    for (int o = 0; (1 << o) < S::LANES; o++) {
+                        const float other = __shfl_down_sync(0xffffffffu, s, 1 << o, S::LANES);
+                        s += same[o] ? other : 0.0f;
+                    }
+                    if (write && leader) {
+                        if (!p.parts)
+                            dg_row[r * p.a.dg.row_stride] = from_f<TG>(s);
+                        else
+                            p.parts[((piece * p.a.B + at.b) * p.a.L + rows.t0 + r) * p.H + rows.gc] = s;
+                    }
+                }
+                if (CARE && edges && here && p.a.dh0) {
+                    const long long m = starts(r);
+                    if (m >= 0)
+#pragma unroll
+                        for (int j = 0; j < V; j++) p.a.dh0[m * p.C + c + j] = e[j];
+                }
+            }
+        };
+        // a warp's lanes sum their heads' gradients together: one way for all of them
+        if (HEAD ? __all_sync(0xffffffffu, fine) : fine)
+            finish(std::false_type{});
+        else
+            finish(std::true_type{});
+        if (packed && at.i == 0) pass_empty(p, p.a.dhT, p.a.dh0, c0, S::WIDTH);
+        if (M::ON) {
+            fence_proxy_async();
+            __syncthreads();
+            if (agent && whole) {
+                const int t0 = rows.chunk * CHUNK;
+                if (!HEAD) tensor_out(&maps.dg, c0, t0, (int)at.b, pg);
+                tensor_out(&maps.dv, c0, t0, (int)at.b, pv);
+                out_close();
+            }
+            phase ^= turn;
+            turn ^= 1;
         }
     }
-    if (packed && at.i == 0) pass_empty(p, p.a.dhT, p.a.dh0, c0, S::WIDTH);
+    if (M::ON && agent) out_done();
 }
 
 // The gate's gradient of heads that span strips: their strips' sums, in order.
@@ -611,7 +971,7 @@ __global__ void scan_step(long long B, int C, int D, int per, const TG *g, long 
     float h = state[slot * C + c];
     for (long long i = i0; i < B; i++) {
         if (i != i0 && (!slots || slots[i] != slot)) continue;
-        const Gate k = open_gate<FORM>(pack_gate<FORM>(to_f(g[i * gs + gc])));
+        const Gate k = gate_of<FORM, false>(to_f(g[i * gs + gc]));
         h = fma0(k.a, h, input_of<FORM>(k, to_f(v[i * vs + c])));
         y[i * ys + c] = from_f<TV>(h);
     }
@@ -633,14 +993,13 @@ size_t elem(int dtype) { return dtype == SPECTRE_F32 ? 4 : 2; }
 
 // The tensors' strips: V = 4 where a head's (or a row's) channels come in fours and every
 // access of four is aligned, else 1.
-template <int V> int strips_of(int C) { return (C + Tile<V>::WIDTH - 1) / Tile<V>::WIDTH; }
-int strips_of(int C, int V) { return V == 4 ? strips_of<4>(C) : strips_of<1>(C); }
-int width_of(int V) { return V == 4 ? Tile<4>::WIDTH : Tile<1>::WIDTH; }
+int width_of(const gated_scan_s *h, int V) { return V == 4 ? 128 / (int)elem(h->dtype) : 32; }
+int strips_of(const gated_scan_s *h, int V) { return (h->C + width_of(h, V) - 1) / width_of(h, V); }
 
 // The most strips that a head's channels lie in.
 int pieces_of(const gated_scan_s *h, int V) {
     if (h->per != GATED_SCAN_PER_HEAD) return 1;
-    const int w = width_of(V);
+    const int w = width_of(h, V);
     if (w % h->D == 0) return 1;
     int most = 1;
     // the first channels of heads within a strip repeat after w heads at the latest
@@ -657,7 +1016,7 @@ struct Work {
 Work work_of(const gated_scan_s *h, long long B, long long L, bool backward, int V) {
     const size_t nchunk = (L + CHUNK - 1) / CHUNK;
     Work w{};
-    if (nchunk > 1) w.words = COUNTER_BYTES + (size_t)B * strips_of(h->C, V) * nchunk * width_of(V) * 8;
+    if (nchunk > 1) w.words = (size_t)B * strips_of(h, V) * nchunk * width_of(h, V) * 8;
     w.words = (w.words + 255) / 256 * 256;
     const int pieces = backward ? pieces_of(h, V) : 1;
     if (pieces > 1) w.parts = (size_t)pieces * B * L * h->H * sizeof(float);
@@ -671,35 +1030,103 @@ size_t workspace(const gated_scan_s *h, long long B, long long L, bool backward)
     return four > one ? four : one;
 }
 
-bool fours(const gated_scan_rows &r, size_t es) {
-    return aligned(r.data, 4 * es) && r.batch_stride % 4 == 0 && r.row_stride % 4 == 0;
+// Rows that tensor copies can move: 16-byte aligned, with strides that are.
+bool sixteens(const gated_scan_rows &r, size_t es, long long B, long long L) {
+    const auto ok = [&](long long n, long long stride) { return n < 2 || (stride > 0 && stride * es % 16 == 0 && stride * es < (1ull << 40)); };
+    return aligned(r.data, 16) && ok(L, r.row_stride) && ok(B, r.batch_stride);
 }
 int vector_of(const gated_scan_s *h, const gated_scan_args *a, bool backward) {
     const bool head = h->per == GATED_SCAN_PER_HEAD;
-    if ((head ? h->D : h->C) % 4) return 1;
+    if ((head ? h->D : h->C) % 4 || a->L > 0x7fffffffLL || a->B > 0x7fffffffLL) return 1;
     const size_t ev = elem(h->dtype), eg = elem(h->gate_dtype);
-    if (!fours(a->v, ev) || (!head && !fours(a->g, eg))) return 1;
-    if (!backward) return fours(a->y, ev) ? 4 : 1;
-    return fours(a->dy, ev) && fours(a->dv, ev) && (head || fours(a->dg, eg)) ? 4 : 1;
+    const auto ok = [&](const gated_scan_rows &r, size_t es) { return sixteens(r, es, a->B, a->L); };
+    if (!ok(a->v, ev) || (!head && !ok(a->g, eg))) return 1;
+    if (!backward) return ok(a->y, ev) ? 4 : 1;
+    return ok(a->dy, ev) && ok(a->dv, ev) && (head || ok(a->dg, eg)) ? 4 : 1;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 find_encode() {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+        cudaGetLastError();
+        return nullptr;
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+}
+
+template <typename T> bool encode(CUtensorMap *m, const gated_scan_rows &r, const Args &p, int width) {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = find_encode();
+    if (!fn) return false;
+    const cuuint64_t es = sizeof(T), line = (p.C * es + 15) / 16 * 16;
+    const cuuint64_t dims[3] = {(cuuint64_t)p.C, (cuuint64_t)p.a.L, (cuuint64_t)p.a.B};
+    // a stride along one row or one batch entry is never used, but has to be a legal one
+    const cuuint64_t strides[2] = {p.a.L > 1 ? (cuuint64_t)r.row_stride * es : line, p.a.B > 1 ? (cuuint64_t)r.batch_stride * es : line};
+    const cuuint32_t box[3] = {(cuuint32_t)width, CHUNK, 1}, step[3] = {1, 1, 1};
+    return fn(m, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, r.data, dims, strides, box, step,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Blocks of a kernel that an SM holds at once, 0 where that cannot be told.
+template <typename K> int resident(K kernel, int threads, int bytes) {
+    int n = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
 }
 
 template <typename TV, typename TG, int FORM, bool HEAD, int V>
 cudaError_t launch_tiles(Args &p, bool backward, const Work &w, cudaStream_t s) {
+    using S = Tile<TV, V>;
+    using M = Stage<TV, TG, HEAD, V>;
     const long long tiles = p.a.B * p.strips * p.nchunk;
+    Maps maps;
+    if (M::ON) {
+        bool ok = HEAD || encode<TG>(&maps.g, p.a.g, p, S::WIDTH);
+        ok = ok && encode<TV>(&maps.v, p.a.v, p, S::WIDTH);
+        if (!backward) {
+            ok = ok && encode<TV>(&maps.y, p.a.y, p, S::WIDTH);
+        } else {
+            ok = ok && encode<TV>(&maps.dy, p.a.dy, p, S::WIDTH) && encode<TV>(&maps.dv, p.a.dv, p, S::WIDTH);
+            ok = ok && (HEAD || encode<TG>(&maps.dg, p.a.dg, p, S::WIDTH));
+        }
+        if (!ok) return cudaErrorInvalidValue;
+    }
     if (w.words) {
-        p.counter = static_cast<unsigned *>(p.a.work);
-        p.words = reinterpret_cast<unsigned long long *>(static_cast<char *>(p.a.work) + COUNTER_BYTES);
+        p.words = static_cast<unsigned long long *>(p.a.work);
         const cudaError_t e = cudaMemsetAsync(p.a.work, 0xff, w.words, s);
         if (e != cudaSuccess) return e;
     }
     if (w.parts) p.parts = reinterpret_cast<float *>(static_cast<char *>(p.a.work) + w.words);
-    if (!backward)
-        scan_forward<TV, TG, FORM, HEAD, V><<<(unsigned)tiles, Tile<V>::THREADS, 0, s>>>(p);
-    else
-        scan_backward<TV, TG, FORM, HEAD, V><<<(unsigned)tiles, Tile<V>::THREADS, 0, s>>>(p);
+    const auto kernel = backward ? scan_backward<TV, TG, FORM, HEAD, V> : scan_forward<TV, TG, FORM, HEAD, V>;
+    const int bytes = M::ON ? 2 * (M::INPUT_BYTES + (backward ? M::V_BYTES : 0)) : 0;
+    // asked for once (every device of this library is of one kind); the attribute is a device's own
+    static const int per_sm[2] = {resident(scan_forward<TV, TG, FORM, HEAD, V>, S::THREADS, M::ON ? 2 * M::INPUT_BYTES : 0),
+                                  resident(scan_backward<TV, TG, FORM, HEAD, V>, S::THREADS, M::ON ? 2 * (M::INPUT_BYTES + M::V_BYTES) : 0)};
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    const long long most = (long long)p.nsm * per_sm[backward];
+    if (!most) return cudaErrorUnknown;
+    cudaLaunchConfig_t config{};
+    config.gridDim = dim3((unsigned)(tiles < most ? tiles : most));
+    config.blockDim = dim3(S::THREADS);
+    config.dynamicSmemBytes = bytes;
+    config.stream = s;
+    cudaLaunchAttribute together{};
+    together.id = cudaLaunchAttributeCooperative;
+    together.val.cooperative = 1;
+    config.attrs = &together;
+    config.numAttrs = p.words ? 1 : 0;   // blocks that wait for one another run at the same time
+    e = cudaLaunchKernelEx(&config, kernel, p, maps);
+    if (e != cudaSuccess) return e;
     if (w.parts) {
         const long long n = p.a.B * p.a.L * p.H;
-        join_parts<TG><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p, Tile<V>::WIDTH);
+        join_parts<TG><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p, S::WIDTH);
     }
     return cudaGetLastError();
 }
@@ -729,7 +1156,7 @@ int run(gated_scan_s *h, const gated_scan_args *a, bool backward, void *stream) 
     // tiles are counted in 31 bits, and every index stays well inside 63
     if (a->L > (1LL << 40) || a->B > (1LL << 31) || nseq > (1LL << 40) / h->C) return SPECTRE_ERR_ARG;
     const long long nchunk = (a->L + CHUNK - 1) / CHUNK;
-    if (nchunk && nchunk * a->B > 0x7fffffffLL / strips_of(h->C, 1)) return SPECTRE_ERR_ARG;
+    if (nchunk && nchunk * a->B > 0x7fffffffLL / strips_of(h, 1)) return SPECTRE_ERR_ARG;
     const int V = vector_of(h, a, backward);
     const Work work = a->L ? work_of(h, a->B, a->L, backward, V) : Work{};
     const size_t ev = elem(h->dtype), eg = elem(h->gate_dtype);
@@ -769,7 +1196,8 @@ int run(gated_scan_s *h, const gated_scan_args *a, bool backward, void *stream) 
     p.H = h->H;
     p.D = h->D;
     p.C = h->C;
-    p.strips = strips_of(h->C, V);
+    p.strips = strips_of(h, V);
+    p.nsm = h->nsm;
     p.nchunk = (int)nchunk;
     p.nseq = nseq;
     return status_of(h->gate == GATED_SCAN_EXP ? launch_types<GATED_SCAN_EXP>(h, p, V, backward, work, s)
