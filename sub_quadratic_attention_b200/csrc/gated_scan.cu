@@ -57,23 +57,32 @@ struct Gate {
 // exp2 and reciprocal (a few units of 2^-24 of the smaller factor, far below the rows' own
 // rounding); a log decay's exp is the accurate one for every type, since its error adds up
 // over as many rows as the state lasts.
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float reciprocal_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <bool FAST> __device__ __forceinline__ float smaller_factor(float g) {
+    if (FAST) {
+        const float e = exp2_approx(fabsf(g) * -1.44269504f);   // -log2(e)
+        return e * reciprocal_approx(1.0f + e);
+    }
+    const float e = expf(-fabsf(g));
+    return e / (1.0f + e);
+}
 template <int FORM, bool FAST> __device__ __forceinline__ Gate gate_of(float g) {
     if (FORM == GATED_SCAN_EXP) return {expf(g), 1.0f};
-    float s;
-    if (FAST) {
-        const float e = __expf(-fabsf(g));
-        s = __fdividef(e, 1.0f + e);
-    } else {
-        const float e = expf(-fabsf(g));
-        s = e / (1.0f + e);
-    }
-    const float o = 1.0f - s;
+    const float s = smaller_factor<FAST>(g), o = 1.0f - s;
     return g >= 0.0f ? Gate{o, s} : Gate{s, o};
 }
 // The same gate in one number: a log decay's a, or the smaller factor with g's sign.
 template <int FORM, bool FAST> __device__ __forceinline__ float pack_gate(float g) {
-    const Gate k = gate_of<FORM, FAST>(g);
-    return FORM == GATED_SCAN_EXP ? k.a : copysignf(g >= 0.0f ? k.c : k.a, g);
+    return FORM == GATED_SCAN_EXP ? expf(g) : copysignf(smaller_factor<FAST>(g), g);
 }
 template <int FORM> __device__ __forceinline__ Gate open_gate(float k) {
     if (FORM == GATED_SCAN_EXP) return {k, 1.0f};
@@ -142,6 +151,13 @@ template <typename T, int V> __device__ __forceinline__ void store(T *p, const f
     for (int j = 0; j < V; j++) r.v[j] = from_f<T>(f[j]);
     *reinterpret_cast<Pack<T, V> *>(p) = r;
 }
+// V neighbouring floats of shared memory, one access
+template <int V> __device__ __forceinline__ void get(const float *p, float (&f)[V]) {
+    const Pack<float, V> r = *reinterpret_cast<const Pack<float, V> *>(p);
+#pragma unroll
+    for (int j = 0; j < V; j++) f[j] = r.v[j];
+}
+template <int V> __device__ __forceinline__ void put(float *p, const float (&f)[V]) { store<float, V>(p, f); }
 
 // One 64-bit word is written and read whole, and everything that a reader needs is in it.
 __device__ __forceinline__ unsigned long long peek(const unsigned long long *p) {
@@ -164,7 +180,7 @@ __device__ __forceinline__ float word_Q(unsigned long long w) { return __uint_as
 // nearest word with P = 0 is among them and nothing is missing before it; tiles ahead that are not
 // done will be, so a block that finds no such word asks again instead of going further back.
 constexpr int REACH = 8;
-template <int WIDTH, int QS> struct LookBack {
+template <int WIDTH, int QS> struct alignas(16) LookBack {
     float state[WIDTH];
     unsigned char seen[QS][WIDTH];
 };
@@ -355,7 +371,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / T
     constexpr bool FAST = sizeof(TV) == 2;
     constexpr bool KEPT = M::ON && !HEAD;   // the gates' products are in shared memory, not in registers
     extern __shared__ __align__(128) char buffers[];
-    __shared__ float sP[S::GROUPS][S::WIDTH], sQ[S::GROUPS][S::WIDTH];
+    __shared__ __align__(16) float sP[S::GROUPS][S::WIDTH], sQ[S::GROUPS][S::WIDTH];
     __shared__ LookBack<S::WIDTH, S::THREADS / S::WIDTH> ahead;
     __shared__ Marks marks;
     __shared__ __align__(8) unsigned long long bars[2];
@@ -424,21 +440,20 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / T
             const TG *gp = rows.template first<TG>(p.a.g, rows.gc);
             const TV *vp = rows.template first<TV>(p.a.v, c);
             // all rows first: what is kept goes where they stand.  A careful walk may be a second
-            // one and reads them from memory again.
+            // one and reads them from memory again, row by row.
             Pack<TG, GV> gs[S::ROWS];
             Pack<TV, V> vs[S::ROWS];
+            if constexpr (!CARE) {
 #pragma unroll
-            for (int r = 0; r < S::ROWS; r++) {
-                if constexpr (!CARE && M::ON) {
-                    if constexpr (HEAD) gs[r].v[0] = g_now[r];
+                for (int r = 0; r < S::ROWS; r++) {
+                    if constexpr (!M::ON) gs[r] = load<TG, GV>(gp + r * p.a.g.row_stride);
+                    else if constexpr (HEAD) gs[r].v[0] = g_now[r];
                     else gs[r] = load<TG, GV>(reinterpret_cast<const TG *>(pg + M::at_g(r)));
-                    vs[r] = load<TV, V>(reinterpret_cast<const TV *>(pv + M::at_v(r)));
-                } else if (r < rows.count) {
-                    gs[r] = load<TG, GV>(gp + r * p.a.g.row_stride);
-                    vs[r] = load<TV, V>(vp + r * p.a.v.row_stride);
+                    if constexpr (!M::ON) vs[r] = load<TV, V>(vp + r * p.a.v.row_stride);
+                    else vs[r] = load<TV, V>(reinterpret_cast<const TV *>(pv + M::at_v(r)));
                 }
+                asm volatile("" ::: "memory");
             }
-            asm volatile("" ::: "memory");
 #pragma unroll
             for (int r = 0; r < S::ROWS; r++) {
                 if (CARE && starts) {
@@ -451,6 +466,10 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / T
                     }
                 }
                 if (!CARE || (r < rows.count && rows.t0 + r >= lo && rows.t0 + r < hi)) {
+                    if constexpr (CARE) {
+                        gs[r] = load<TG, GV>(gp + r * p.a.g.row_stride);
+                        vs[r] = load<TV, V>(vp + r * p.a.v.row_stride);
+                    }
                     const Pack<TG, GV> &g = gs[r];
                     const Pack<TV, V> &v = vs[r];
                     Gate k[GV];
@@ -486,10 +505,15 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / T
             for (int j = 0; j < V; j++) fine &= finite(Q[S::ROWS - 1][j]);
         }
         if (!fine) walk(std::true_type{});
+        {
+            float lp[V], lq[V];
 #pragma unroll
-        for (int j = 0; j < V; j++) {
-            sP[group][lane * V + j] = lastP[HEAD ? 0 : j];
-            sQ[group][lane * V + j] = arrived ? Q[S::ROWS - 1][j] : __uint_as_float(0x7fc00000u);
+            for (int j = 0; j < V; j++) {
+                lp[j] = lastP[HEAD ? 0 : j];
+                lq[j] = arrived ? Q[S::ROWS - 1][j] : __uint_as_float(0x7fc00000u);
+            }
+            put(&sP[group][lane * V], lp);
+            put(&sQ[group][lane * V], lq);
         }
         __syncthreads();
 
@@ -525,48 +549,58 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / T
         }
 
         float h0[V];
-        fine = true;
+        fine = rows.count == S::ROWS;
+        {
+            float gp[V], gq[V], state[V];
+            get(&sP[group][lane * V], gp);
+            get(&sQ[group][lane * V], gq);
+            get(&ahead.state[lane * V], state);
 #pragma unroll
-        for (int j = 0; j < V; j++) {
-            h0[j] = fma0(sP[group][lane * V + j], ahead.state[lane * V + j], sQ[group][lane * V + j]);
-            fine &= finite(h0[j]);
+            for (int j = 0; j < V; j++) {
+                h0[j] = fma0(gp[j], state[j], gq[j]);
+                fine &= finite(h0[j]);
+            }
         }
         const long long tile0 = (long long)at.i * CHUNK;
         const bool whole = !packed || (tile0 >= lo && tile0 + CHUNK <= hi);   // the tile's rows are all written, or do not exist
-        TV *y = rows.template first<TV>(p.a.y, c);
+        auto finish = [&](auto careful) {
+            constexpr bool CARE = decltype(careful)::value;
+            TV *y = rows.template first<TV>(p.a.y, c);
 #pragma unroll
-        for (int r = 0; r < S::ROWS; r++) {
-            if (r >= rows.count) break;
-            float h[V], pr[M::ON && !HEAD ? 4 : GV];
-            if constexpr (KEPT) {
-                M::kept(pg, pv, r, pr);
-            } else {
+            for (int r = 0; r < S::ROWS; r++) {
+                if (CARE && r >= rows.count) break;
+                float h[V], pr[M::ON && !HEAD ? 4 : GV];
+                if constexpr (KEPT) {
+                    M::kept(pg, pv, r, pr);
+                } else {
 #pragma unroll
-                for (int j = 0; j < GV; j++) pr[j] = P[r][j];
+                    for (int j = 0; j < GV; j++) pr[j] = P[r][j];
+                }
+#pragma unroll
+                for (int j = 0; j < V; j++) h[j] = fma_if<CARE>(pr[HEAD ? 0 : j], h0[j], Q[r][j]);
+                const bool in = !CARE || (rows.t0 + r >= lo && rows.t0 + r < hi);
+                if (CARE && ends && in && p.a.hT) {
+                    const long long n = packed ? marks.last[group * S::ROWS + r] : rows.t0 + r == p.a.L - 1 ? at.b : -1;
+                    if (n >= 0)
+#pragma unroll
+                        for (int j = 0; j < V; j++) p.a.hT[n * p.C + c + j] = h[j];
+                }
+                if (M::ON && (!CARE || whole)) {
+                    store<TV, V>(reinterpret_cast<TV *>(pv + M::at_v(r)), h);
+                    continue;
+                }
+                if (!in) {
+                    if (!p.a.zero_outside) continue;
+#pragma unroll
+                    for (int j = 0; j < V; j++) h[j] = 0.0f;
+                }
+                store<TV, V>(y + r * p.a.y.row_stride, h);
             }
-#pragma unroll
-            for (int j = 0; j < V; j++) h[j] = fmaf(pr[HEAD ? 0 : j], h0[j], Q[r][j]);
-            if (!fine)
-#pragma unroll
-                for (int j = 0; j < V; j++) h[j] = fma0(pr[HEAD ? 0 : j], h0[j], Q[r][j]);
-            const bool in = all_in || (rows.t0 + r >= lo && rows.t0 + r < hi);
-            if (ends && in && p.a.hT) {
-                const long long n = packed ? marks.last[group * S::ROWS + r] : rows.t0 + r == p.a.L - 1 ? at.b : -1;
-                if (n >= 0)
-#pragma unroll
-                    for (int j = 0; j < V; j++) p.a.hT[n * p.C + c + j] = h[j];
-            }
-            if (M::ON && whole) {
-                store<TV, V>(reinterpret_cast<TV *>(pv + M::at_v(r)), h);
-                continue;
-            }
-            if (!in) {
-                if (!p.a.zero_outside) continue;
-#pragma unroll
-                for (int j = 0; j < V; j++) h[j] = 0.0f;
-            }
-            store<TV, V>(y + r * p.a.y.row_stride, h);
-        }
+        };
+        if (fine && whole && !ends)
+            finish(std::false_type{});
+        else
+            finish(std::true_type{});
         if (packed && at.i == 0) pass_empty(p, p.a.h0, p.a.hT, c0, S::WIDTH);
         if (M::ON) {
             fence_proxy_async();
@@ -600,8 +634,8 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
     constexpr bool IN_PLACE = M::ON && !HEAD;   // the groups' P stand where their gates were
     extern __shared__ __align__(128) char buffers[];
     // (P, Q) of the states going forward, (R, E) of the gradients going back
-    __shared__ float sP[IN_PLACE ? 1 : S::GROUPS][S::WIDTH], sQ[S::GROUPS][S::WIDTH];
-    __shared__ float sR[S::GROUPS][S::WIDTH], sE[S::GROUPS][S::WIDTH];
+    __shared__ __align__(16) float sP[IN_PLACE ? 1 : S::GROUPS][S::WIDTH], sQ[S::GROUPS][S::WIDTH];
+    __shared__ __align__(16) float sR[S::GROUPS][S::WIDTH], sE[S::GROUPS][S::WIDTH];
     __shared__ LookBack<S::WIDTH, S::THREADS / S::WIDTH> ahead;
     __shared__ Marks marks;
     __shared__ __align__(8) unsigned long long bars[2];
@@ -762,20 +796,22 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
         }
         if (!fine) walk(std::true_type{});
 #pragma unroll
-        for (int j = 0; j < V; j++) {
-            sQ[group][lane * V + j] = Q[j];
-            sR[group][lane * V + j] = T[j];
-            sE[group][lane * V + j] = arrived ? E[j] : __uint_as_float(0x7fc00000u);
-        }
+        for (int j = 0; j < V; j++) E[j] = arrived ? E[j] : __uint_as_float(0x7fc00000u);
+        put(&sQ[group][lane * V], Q);
+        put(&sR[group][lane * V], T);
+        put(&sE[group][lane * V], E);
         if constexpr (IN_PLACE) {
             // float4 in the first row's gates, or a half in each of the first two
             float *a = reinterpret_cast<float *>(pg + M::at_g(0)), *b = reinterpret_cast<float *>(pg + M::at_g(1));
             asm volatile("" ::: "memory");   // the gates have been read
-#pragma unroll
-            for (int j = 0; j < 4; j++) (sizeof(TG) == 4 || j < 2 ? a[j] : b[j - 2]) = P[j];
+            if constexpr (sizeof(TG) == 4) {
+                *reinterpret_cast<float4 *>(a) = make_float4(P[0], P[1], P[2], P[3]);
+            } else {
+                *reinterpret_cast<float2 *>(a) = make_float2(P[0], P[1]);
+                *reinterpret_cast<float2 *>(b) = make_float2(P[2], P[3]);
+            }
         } else {
-#pragma unroll
-            for (int j = 0; j < V; j++) sP[group][lane * V + j] = P[j];
+            put(&sP[group][lane * V], P);
         }
         __syncthreads();
 
@@ -824,15 +860,22 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
 
         const bool whole = !packed || (tile0 >= lo && tile0 + CHUNK <= hi);   // the tile's rows are all written, or do not exist
         float h[V], e[V];
+        {
+            float gt[V], ge[V], grad[V];
+            get(&sQ[group][lane * V], h);
+            get(&sR[group][lane * V], gt);
+            get(&sE[group][lane * V], ge);
+            get(&ahead.state[lane * V], grad);
 #pragma unroll
-        for (int j = 0; j < V; j++) {
-            h[j] = sQ[group][lane * V + j];
-            e[j] = fma0(sR[group][lane * V + j], ahead.state[lane * V + j], sE[group][lane * V + j]);
-            fine &= finite(h[j]) && finite(e[j]);
+            for (int j = 0; j < V; j++) {
+                e[j] = fma0(gt[j], grad[j], ge[j]);
+                fine &= finite(h[j]) && finite(e[j]);
+            }
         }
         // lanes of one head: lane + 2^o is still in it
         bool same[5], leader = true;
-        if (HEAD) {
+        const bool one_head = HEAD && p.D % S::WIDTH == 0;   // in every strip
+        if (HEAD && !one_head) {
 #pragma unroll
             for (int o = 0; o < 5; o++) {
                 const int other = c + (V << o);
@@ -864,6 +907,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
             }
             asm volatile("" ::: "memory");   // dv goes where the values were
             TV *dv_row = rows.template first<TV>(p.a.dv, c);
+            float head[HEAD ? S::ROWS : 1];
             TG *dg_row = rows.template first<TG>(p.a.dg, rows.gc);
 #pragma unroll
             for (int r = S::ROWS - 1; r >= 0; r--) {
@@ -884,7 +928,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
                     dv[j] = !here ? 0.0f : FORM == GATED_SCAN_EXP ? dh : mul_if<CARE>(q.c, dh);
                     e[j] = mul_if<CARE>(q.a, dh);
                 }
-                // straight to memory: rows of tiles that are not whole, one by one
+                // rows of tiles that are not whole go straight to memory
                 const bool write = here || (r < rows.count && p.a.zero_outside);
                 if (M::ON && whole)
                     store<TV, V>(reinterpret_cast<TV *>(pv + M::at_v(r)), dv);
@@ -896,26 +940,57 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
                     else if (write)
                         store<TG, V>(dg_row + r * p.a.dg.row_stride, dg);
                 } else {
-                    float s = 0.0f;
+                    head[r] = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < V; j++) s += dg[j];
-#pragma unroll
-                    for (int o = 0; (1 << o) < S::LANES; o++) {
-                        const float other = __shfl_down_sync(0xffffffffu, s, 1 << o, S::LANES);
-                        s += same[o] ? other : 0.0f;
-                    }
-                    if (write && leader) {
-                        if (!p.parts)
-                            dg_row[r * p.a.dg.row_stride] = from_f<TG>(s);
-                        else
-                            p.parts[((piece * p.a.B + at.b) * p.a.L + rows.t0 + r) * p.H + rows.gc] = s;
-                    }
+                    for (int j = 0; j < V; j++) head[r] += dg[j];
                 }
                 if (CARE && edges && here && p.a.dh0) {
                     const long long m = starts(r);
                     if (m >= 0)
 #pragma unroll
                         for (int j = 0; j < V; j++) p.a.dh0[m * p.C + c + j] = e[j];
+                }
+            }
+            if constexpr (HEAD) {
+                // the sums over a head's lanes
+                auto write = [&](int r, float sum) {
+                    const bool here = !CARE || in(r);
+                    if (!here && !(r < rows.count && p.a.zero_outside)) return;
+                    if (!p.parts)
+                        dg_row[r * p.a.dg.row_stride] = from_f<TG>(sum);
+                    else
+                        p.parts[((piece * p.a.B + at.b) * p.a.L + rows.t0 + r) * p.H + rows.gc] = sum;
+                };
+                if (one_head) {
+                    // halving: each exchange leaves a lane half of its rows, until it has one (or its share of one)
+#pragma unroll
+                    for (int o = S::LANES / 2, n = S::ROWS; o > 0; o >>= 1) {
+                        if (n > 1) {
+                            n >>= 1;
+#pragma unroll
+                            for (int r = 0; r < n; r++) {
+                                const bool up = lane & o;
+                                const float give = up ? head[r] : head[r + n], stay = up ? head[r + n] : head[r];
+                                head[r] = stay + __shfl_xor_sync(0xffffffffu, give, o, S::LANES);
+                            }
+                        } else {
+                            head[0] += __shfl_xor_sync(0xffffffffu, head[0], o, S::LANES);
+                        }
+                    }
+                    constexpr int SHARE = S::LANES / S::ROWS > 0 ? S::LANES / S::ROWS : 1;   // lanes with the same row
+                    if (lane % SHARE == 0)
+                        if (rows.mine) write(lane / SHARE, head[0]);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < S::ROWS; r++) {
+                        float sum = head[r];
+#pragma unroll
+                        for (int o = 0; (1 << o) < S::LANES; o++) {
+                            const float other = __shfl_down_sync(0xffffffffu, sum, 1 << o, S::LANES);
+                            sum += same[o] ? other : 0.0f;
+                        }
+                        if (leader) write(r, sum);
+                    }
                 }
             }
         };
