@@ -47,6 +47,19 @@ using namespace rows_io;
 
 constexpr int CHUNK = GATED_SCAN_CHUNK;
 
+template <typename T, int V> struct alignas(sizeof(T) * V) Pack {
+    T v[V];
+};
+template <typename T, int V> __device__ __forceinline__ Pack<T, V> load(const T *p) {
+    return *reinterpret_cast<const Pack<T, V> *>(p);
+}
+template <typename T, int V> __device__ __forceinline__ void store(T *p, const float *f) {
+    Pack<T, V> r;
+#pragma unroll
+    for (int j = 0; j < V; j++) r.v[j] = from_f<T>(f[j]);
+    *reinterpret_cast<Pack<T, V> *>(p) = r;
+}
+
 struct Gate {
     float a, c;   // h = a h + c v
 };
@@ -80,25 +93,144 @@ template <int FORM, bool FAST> __device__ __forceinline__ Gate gate_of(float g) 
     const float s = smaller_factor<FAST>(g), o = 1.0f - s;
     return g >= 0.0f ? Gate{o, s} : Gate{s, o};
 }
-// The same gate in one number: a log decay's a, or the smaller factor with g's sign.
-template <int FORM, bool FAST> __device__ __forceinline__ float pack_gate(float g) {
-    return FORM == GATED_SCAN_EXP ? expf(g) : copysignf(smaller_factor<FAST>(g), g);
+
+// Two fp32 operations an instruction where a thread has channels in fours.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 r, a, b, c;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
 }
-template <int FORM> __device__ __forceinline__ Gate open_gate(float k) {
-    if (FORM == GATED_SCAN_EXP) return {k, 1.0f};
-    const float s = fabsf(k), o = 1.0f - s;
-    return signbit(k) ? Gate{s, o} : Gate{o, s};
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 r, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 r, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+template <int V> __device__ __forceinline__ void fma_all(float (&r)[V], const float (&a)[V], const float (&b)[V], const float (&c)[V]) {
+    if constexpr (V == 4) {
+        const float2 x = fma2({a[0], a[1]}, {b[0], b[1]}, {c[0], c[1]}), y = fma2({a[2], a[3]}, {b[2], b[3]}, {c[2], c[3]});
+        r[0] = x.x, r[1] = x.y, r[2] = y.x, r[3] = y.y;
+    } else {
+        r[0] = fmaf(a[0], b[0], c[0]);
+    }
+}
+template <int V> __device__ __forceinline__ void mul_all(float (&r)[V], const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V == 4) {
+        const float2 x = mul2({a[0], a[1]}, {b[0], b[1]}), y = mul2({a[2], a[3]}, {b[2], b[3]});
+        r[0] = x.x, r[1] = x.y, r[2] = y.x, r[3] = y.y;
+    } else {
+        r[0] = a[0] * b[0];
+    }
+}
+template <int V> __device__ __forceinline__ void add_all(float (&r)[V], const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V == 4) {
+        const float2 x = add2({a[0], a[1]}, {b[0], b[1]}), y = add2({a[2], a[3]}, {b[2], b[3]});
+        r[0] = x.x, r[1] = x.y, r[2] = y.x, r[3] = y.y;
+    } else {
+        r[0] = a[0] + b[0];
+    }
+}
+template <int V> __device__ __forceinline__ void fill(float (&r)[V], float f) {
+#pragma unroll
+    for (int j = 0; j < V; j++) r[j] = f;
+}
+template <int N, typename T, int V> __device__ __forceinline__ void floats(float (&f)[N], const Pack<T, V> &x) {
+    static_assert(N == V, "");
+#pragma unroll
+    for (int j = 0; j < V; j++) f[j] = to_f(x.v[j]);
+}
+
+// N gates at once.  For bf16 rows c = 1 / (1 + exp(g)) to its own relative precision, and
+// a = 1 - c, or exp(g) c where that is the smaller.
+template <int FORM, bool FAST, int N> __device__ __forceinline__ void gates(const float (&g)[N], float (&a)[N], float (&c)[N]) {
+    if constexpr (FORM == GATED_SCAN_SIGMOID && FAST) {
+        float k[N], e[N], one[N], d[N], small[N];
+        fill(k, 1.44269504f);   // log2(e)
+        fill(one, 1.0f);
+        mul_all(k, g, k);
+#pragma unroll
+        for (int j = 0; j < N; j++) e[j] = exp2_approx(k[j]);
+        add_all(d, e, one);
+#pragma unroll
+        for (int j = 0; j < N; j++) c[j] = reciprocal_approx(d[j]);
+        mul_all(small, e, c);
+        fill(d, -1.0f);
+        fma_all(a, c, d, one);
+#pragma unroll
+        for (int j = 0; j < N; j++) a[j] = c[j] <= 0.5f ? a[j] : small[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+            const Gate q = gate_of<FORM, FAST>(g[j]);
+            a[j] = q.a;
+            c[j] = q.c;
+        }
+    }
+}
+// The same gates, each in one number: a log decay's a, or the smaller factor with g's sign.
+template <int FORM, bool FAST, int N> __device__ __forceinline__ void pack_gates(const float (&g)[N], float (&k)[N]) {
+    if constexpr (FORM == GATED_SCAN_EXP) {
+#pragma unroll
+        for (int j = 0; j < N; j++) k[j] = expf(g[j]);
+    } else if constexpr (!FAST) {
+#pragma unroll
+        for (int j = 0; j < N; j++) k[j] = copysignf(smaller_factor<false>(g[j]), g[j]);
+    } else {
+        float e[N], one[N], d[N];
+        fill(d, -1.44269504f);
+        fill(one, 1.0f);
+#pragma unroll
+        for (int j = 0; j < N; j++) e[j] = fabsf(g[j]);
+        mul_all(e, e, d);
+#pragma unroll
+        for (int j = 0; j < N; j++) e[j] = exp2_approx(e[j]);
+        add_all(d, e, one);
+#pragma unroll
+        for (int j = 0; j < N; j++) d[j] = reciprocal_approx(d[j]);
+        mul_all(k, e, d);
+#pragma unroll
+        for (int j = 0; j < N; j++) k[j] = copysignf(k[j], g[j]);
+    }
+}
+template <int FORM, int N> __device__ __forceinline__ void open_gates(const float (&k)[N], float (&a)[N], float (&c)[N]) {
+    if constexpr (FORM == GATED_SCAN_EXP) {
+#pragma unroll
+        for (int j = 0; j < N; j++) a[j] = k[j], c[j] = 1.0f;
+    } else {
+        float s[N], one[N], o[N];
+        fill(one, 1.0f);
+#pragma unroll
+        for (int j = 0; j < N; j++) s[j] = -fabsf(k[j]);
+        add_all(o, s, one);
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+            a[j] = signbit(k[j]) ? -s[j] : o[j];
+            c[j] = signbit(k[j]) ? o[j] : -s[j];
+        }
+    }
+}
+template <int V, int N> __device__ __forceinline__ void spread(float (&r)[V], const float (&x)[N]) {   // a head's for its channels
+#pragma unroll
+    for (int j = 0; j < V; j++) r[j] = x[N == 1 ? 0 : j];
 }
 template <int FORM> constexpr float HOLD = FORM == GATED_SCAN_EXP ? 1.0f : 0.0f;   // packed: a = 1
 
 // a * h where a factor of zero takes h out, NaN and infinities included
 __device__ __forceinline__ float mul0(float a, float h) { return a == 0.0f ? 0.0f : a * h; }
 __device__ __forceinline__ float fma0(float a, float h, float b) { return a == 0.0f ? b : fmaf(a, h, b); }
-// the same where h is known to be finite, or where NaN only tells that it was not
-template <bool GUARD> __device__ __forceinline__ float fma_if(float a, float h, float b) {
-    return GUARD ? fma0(a, h, b) : fmaf(a, h, b);
-}
-template <bool GUARD> __device__ __forceinline__ float mul_if(float a, float h) { return GUARD ? mul0(a, h) : a * h; }
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __int_as_float(0x7f800000); }
 
 template <int FORM> __device__ __forceinline__ float input_of(Gate k, float v) {
@@ -120,7 +252,8 @@ template <typename TV, int V> struct Tile {
     static constexpr int THREADS = LANES * GROUPS;
 };
 
-// Workspace: one word for each tile and channel, all ones before a run.
+// Workspace: one word for each tile and channel, all ones before a run, and as many words ahead of
+// the first as a look back may ask for.
 constexpr unsigned long long NOTHING = ~0ull;
 constexpr unsigned MOST_POLLS = 1u << 22;   // of about a microsecond each
 
@@ -139,18 +272,6 @@ template <typename T> __device__ __forceinline__ T *row(const gated_scan_rows &r
     return static_cast<T *>(r.data) + b * r.batch_stride + t * r.row_stride;
 }
 
-template <typename T, int V> struct alignas(sizeof(T) * V) Pack {
-    T v[V];
-};
-template <typename T, int V> __device__ __forceinline__ Pack<T, V> load(const T *p) {
-    return *reinterpret_cast<const Pack<T, V> *>(p);
-}
-template <typename T, int V> __device__ __forceinline__ void store(T *p, const float *f) {
-    Pack<T, V> r;
-#pragma unroll
-    for (int j = 0; j < V; j++) r.v[j] = from_f<T>(f[j]);
-    *reinterpret_cast<Pack<T, V> *>(p) = r;
-}
 // V neighbouring floats of shared memory, one access
 template <int V> __device__ __forceinline__ void get(const float *p, float (&f)[V]) {
     const Pack<float, V> r = *reinterpret_cast<const Pack<float, V> *>(p);
@@ -180,6 +301,7 @@ __device__ __forceinline__ float word_Q(unsigned long long w) { return __uint_as
 // nearest word with P = 0 is among them and nothing is missing before it; tiles ahead that are not
 // done will be, so a block that finds no such word asks again instead of going further back.
 constexpr int REACH = 8;
+constexpr int AHEAD = 64;   // the most tiles that all threads of a block ask for
 template <int WIDTH, int QS> struct alignas(16) LookBack {
     float state[WIDTH];
     unsigned char seen[QS][WIDTH];
@@ -191,17 +313,17 @@ __device__ __forceinline__ void look_back(LookBack<WIDTH, QS> &m, const unsigned
     for (unsigned polls = 0;; polls++) {
         const int qs = far || polls ? QS : 1;
         if (q < qs) {
-            const int last = i - 1 - q * REACH;
+            // words ahead of tile 0 belong to others, or to nobody: tile 0's comes before them
+            const unsigned long long *from = words + (long long)(i - 1 - q * REACH) * WIDTH + x;
 #pragma unroll
-            for (int j = 0; j < REACH; j++) w[j] = mine && last - j >= 0 ? peek(words + (long long)(last - j) * WIDTH + x) : 0;
+            for (int j = 0; j < REACH; j++) w[j] = peek(from - j * WIDTH);
             int seen = REACH;       // how many pairs come before a word with P = 0; one more: a word is missing
 #pragma unroll
             for (int j = REACH - 1; j >= 0; j--) {
-                if (w[j] == NOTHING)
-                    seen = REACH + 1;
-                else if (word_P(w[j]) == 0.0f)
-                    seen = j;
+                const unsigned P = (unsigned)(w[j] >> 32);
+                seen = P == (unsigned)(NOTHING >> 32) ? REACH + 1 : P == 0 ? j : seen;
             }
+            if (!mine) seen = 0;
             m.seen[q][x] = (unsigned char)seen;
         }
         __syncthreads();
@@ -229,20 +351,27 @@ __device__ __forceinline__ void look_back(LookBack<WIDTH, QS> &m, const unsigned
 }
 
 // Where the block's tile lies.  Tiles are numbered chunk by chunk over all batch entries and
-// strips, in the direction of the walk, so that every strip advances at the same time.
+// strips, in the direction of the walk, so that every strip advances at the same time; a block
+// takes every gridDim.x-th, and goes from one to the next without a division.
 struct Place {
-    int i, strip;        // chunk in walking order
-    long long b, tile;   // tile: the strip's first word
+    int i, b, strip;   // i: the chunk in walking order
+    __device__ __forceinline__ Place() {}
+    __device__ __forceinline__ Place(const Args &p, unsigned ticket) {
+        const unsigned strips = p.strips, per = (unsigned)p.a.B * strips, rest = ticket % per;
+        i = (int)(ticket / per);
+        b = (int)(rest / strips);
+        strip = (int)(rest % strips);
+    }
+    __device__ __forceinline__ void advance(const Args &p, const Place &by) {
+        strip += by.strip;
+        b += by.b;
+        i += by.i;
+        if (strip >= p.strips) strip -= p.strips, b++;
+        if (b >= (int)p.a.B) b -= (int)p.a.B, i++;
+    }
+    __device__ __forceinline__ long long first_word(const Args &p) const { return ((long long)b * p.strips + strip) * p.nchunk; }
 };
-__device__ __forceinline__ Place place_of(const Args &p, unsigned ticket) {
-    const unsigned per = (unsigned)(p.a.B * p.strips), i = ticket / per, rest = ticket - i * per;
-    Place t;
-    t.i = (int)i;
-    t.b = rest / p.strips;
-    t.strip = (int)(rest - (unsigned)t.b * p.strips);
-    t.tile = (t.b * p.strips + t.strip) * p.nchunk;
-    return t;
-}
+
 // Packed rows: the sequence that starts at, and that ends with, each row of the tile (or -1),
 // and the rows that lie in sequences at all.
 struct Marks {
@@ -345,8 +474,7 @@ template <typename TV, typename TG, bool HEAD, int V> struct Rows {
     bool mine;
     long long t0;
     int count;   // rows before the tensor's end, 0 to ROWS
-    __device__ Rows(const Args &p, unsigned ticket, bool backward) {
-        at = place_of(p, ticket);
+    __device__ Rows(const Args &p, const Place &place, bool backward) : at(place) {
         chunk = backward ? p.nchunk - 1 - at.i : at.i;
         c0 = at.strip * S::WIDTH;
         c = c0 + threadIdx.x % S::LANES * V;
@@ -377,14 +505,14 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / T
     __shared__ __align__(8) unsigned long long bars[2];
     const bool packed = p.a.cu_seqlens != nullptr;
     const int lane = threadIdx.x % S::LANES, group = threadIdx.x / S::LANES;
-    const unsigned tiles = (unsigned)(p.a.B * p.strips) * p.nchunk;
+    Place next(p, blockIdx.x);
+    const Place by(p, gridDim.x);
     // more tiles of a strip in flight than one thread's REACH: ask far at once
     const bool far = (unsigned)(p.a.B * p.strips) * REACH < gridDim.x;
 
     const bool agent = threadIdx.x == S::THREADS - 32;   // issues all copies
-    auto fetch = [&](unsigned ticket, int turn) {
-        if (!M::ON || !agent || ticket >= tiles) return;
-        const Place at = place_of(p, ticket);
+    auto fetch = [&](const Place &at, int turn) {
+        if (!M::ON || !agent || at.i >= p.nchunk) return;
         char *to = buffers + turn * M::INPUT_BYTES;
         const uint32_t bar = smem_u32(&bars[turn]);
         mbar_arrive_expect_tx(bar, M::INPUT_BYTES);
@@ -393,9 +521,9 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / T
     };
     // one gate a row is too little for a copy: it waits in a register
     TG g_now[HEAD ? S::ROWS : 1];
-    auto fetch_gates = [&](unsigned ticket) {
-        if (!HEAD || !M::ON || ticket >= tiles) return;
-        const R rows(p, ticket, false);
+    auto fetch_gates = [&](const Place &at) {
+        if (!HEAD || !M::ON || at.i >= p.nchunk) return;
+        const R rows(p, at, false);
         const TG *g = rows.template first<TG>(p.a.g, rows.gc);
 #pragma unroll
         for (int r = 0; r < (HEAD ? S::ROWS : 1); r++)
@@ -407,14 +535,16 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / T
             mbar_init(smem_u32(&bars[1]), 1);
         }
         __syncthreads();
-        fetch(blockIdx.x, 0);
-        fetch_gates(blockIdx.x);
+        fetch(next, 0);
+        fetch_gates(next);
     }
     int turn = 0;
     uint32_t phase = 0;
-    for (unsigned ticket = blockIdx.x; ticket < tiles; ticket += gridDim.x) {
+    while (next.i < p.nchunk) {
+        const Place now = next;
+        next.advance(p, by);
         char *const pg = buffers + turn * M::INPUT_BYTES, *const pv = pg + M::G_BYTES;
-        const R rows(p, ticket, false);
+        const R rows(p, now, false);
         const Place &at = rows.at;
         const int c0 = rows.c0, c = rows.c;
         long long lo = 0, hi = p.a.L;
@@ -472,17 +602,20 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / T
                     }
                     const Pack<TG, GV> &g = gs[r];
                     const Pack<TV, V> &v = vs[r];
-                    Gate k[GV];
+                    float gf[GV], vf[V], ka[GV], kc[GV];
+                    floats(gf, g);
+                    floats(vf, v);
+                    gates<FORM, FAST>(gf, ka, kc);
+                    mul_all(lastP, lastP, ka);
+                    float a[V], c[V];
+                    spread(a, ka);
+                    spread(c, kc);
+                    if constexpr (CARE) {
 #pragma unroll
-                    for (int j = 0; j < GV; j++) {
-                        k[j] = gate_of<FORM, FAST>(to_f(g.v[j]));
-                        lastP[j] *= k[j].a;
-                    }
-#pragma unroll
-                    for (int j = 0; j < V; j++) {
-                        const Gate &kj = k[HEAD ? 0 : j];
-                        const float vj = to_f(v.v[j]);
-                        q[j] = fma_if<CARE>(kj.a, q[j], FORM == GATED_SCAN_EXP ? vj : mul_if<CARE>(kj.c, vj));
+                        for (int j = 0; j < V; j++) q[j] = fma0(a[j], q[j], FORM == GATED_SCAN_EXP ? vf[j] : mul0(c[j], vf[j]));
+                    } else {
+                        if (FORM == GATED_SCAN_SIGMOID) mul_all(vf, c, vf);
+                        fma_all(q, a, q, vf);
                     }
                 }
                 if constexpr (KEPT)
@@ -518,10 +651,10 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / T
         __syncthreads();
 
         if (M::ON && agent) out_read();   // the other buffer's rows of y have left it
-        fetch(ticket + gridDim.x, turn ^ 1);
-        fetch_gates(ticket + gridDim.x);
+        fetch(next, turn ^ 1);
+        fetch_gates(next);
         const int x = threadIdx.x, cx = c0 + threadIdx.x % S::WIDTH;
-        unsigned long long *const words = p.words + at.tile * S::WIDTH;
+        unsigned long long *const words = p.words + at.first_word(p) * S::WIDTH;
         const bool more = at.i + 1 < p.nchunk;
         float allP = 1.0f, allQ = 0.0f;
         if (x < S::WIDTH) {
@@ -569,15 +702,15 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / T
 #pragma unroll
             for (int r = 0; r < S::ROWS; r++) {
                 if (CARE && r >= rows.count) break;
-                float h[V], pr[M::ON && !HEAD ? 4 : GV];
-                if constexpr (KEPT) {
-                    M::kept(pg, pv, r, pr);
+                float h[V], pr[V];
+                if constexpr (KEPT) M::kept(pg, pv, r, pr);
+                else spread(pr, P[r]);
+                if constexpr (CARE) {
+#pragma unroll
+                    for (int j = 0; j < V; j++) h[j] = fma0(pr[j], h0[j], Q[r][j]);
                 } else {
-#pragma unroll
-                    for (int j = 0; j < GV; j++) pr[j] = P[r][j];
+                    fma_all(h, pr, h0, Q[r]);
                 }
-#pragma unroll
-                for (int j = 0; j < V; j++) h[j] = fma_if<CARE>(pr[HEAD ? 0 : j], h0[j], Q[r][j]);
                 const bool in = !CARE || (rows.t0 + r >= lo && rows.t0 + r < hi);
                 if (CARE && ends && in && p.a.hT) {
                     const long long n = packed ? marks.last[group * S::ROWS + r] : rows.t0 + r == p.a.L - 1 ? at.b : -1;
@@ -641,13 +774,13 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
     __shared__ __align__(8) unsigned long long bars[2];
     const bool packed = p.a.cu_seqlens != nullptr;
     const int lane = threadIdx.x % S::LANES, group = threadIdx.x / S::LANES;
-    const unsigned tiles = (unsigned)(p.a.B * p.strips) * p.nchunk;
+    Place next(p, blockIdx.x);
+    const Place by(p, gridDim.x);
     const bool far = (unsigned)(p.a.B * p.strips) * REACH < gridDim.x;
 
     const bool agent = threadIdx.x == S::THREADS - 32;   // issues all copies
-    auto fetch = [&](unsigned ticket, int turn) {
-        if (!M::ON || !agent || ticket >= tiles) return;
-        const Place at = place_of(p, ticket);
+    auto fetch = [&](const Place &at, int turn) {
+        if (!M::ON || !agent || at.i >= p.nchunk) return;
         char *to = buffers + turn * TILE_BYTES;
         const uint32_t bar = smem_u32(&bars[turn]);
         const int c0 = at.strip * S::WIDTH, t0 = (p.nchunk - 1 - at.i) * CHUNK;
@@ -657,9 +790,9 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
         tensor_in(to + M::INPUT_BYTES, &maps.dy, c0, t0, (int)at.b, bar);
     };
     TG g_now[HEAD ? S::ROWS : 1];
-    auto fetch_gates = [&](unsigned ticket) {
-        if (!HEAD || !M::ON || ticket >= tiles) return;
-        const R rows(p, ticket, true);
+    auto fetch_gates = [&](const Place &at) {
+        if (!HEAD || !M::ON || at.i >= p.nchunk) return;
+        const R rows(p, at, true);
         const TG *g = rows.template first<TG>(p.a.g, rows.gc);
 #pragma unroll
         for (int r = 0; r < (HEAD ? S::ROWS : 1); r++)
@@ -671,14 +804,16 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
             mbar_init(smem_u32(&bars[1]), 1);
         }
         __syncthreads();
-        fetch(blockIdx.x, 0);
-        fetch_gates(blockIdx.x);
+        fetch(next, 0);
+        fetch_gates(next);
     }
     int turn = 0;
     uint32_t phase = 0;
-    for (unsigned ticket = blockIdx.x; ticket < tiles; ticket += gridDim.x) {
+    while (next.i < p.nchunk) {
+        const Place now = next;
+        next.advance(p, by);
         char *const pg = buffers + turn * TILE_BYTES, *const pv = pg + M::G_BYTES, *const pd = pg + M::INPUT_BYTES;
-        const R rows(p, ticket, true);
+        const R rows(p, now, true);
         const Place &at = rows.at;
         const int c0 = rows.c0, c = rows.c;
         const long long tile0 = (long long)rows.chunk * CHUNK;
@@ -728,31 +863,42 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
                         own_d[r] = load<TV, V>(dp + r * p.a.dy.row_stride);
                     }
                 }
+                float gf[GV];
+                floats(gf, g);
+                pack_gates<FORM, FAST>(gf, k[r]);
 #pragma unroll
-                for (int j = 0; j < GV; j++) k[r][j] = there ? pack_gate<FORM, FAST>(to_f(g.v[j])) : HOLD<FORM>;
+                for (int j = 0; j < GV; j++) k[r][j] = there ? k[r][j] : HOLD<FORM>;
             }
         }
         // row r of values or dy; rows that are missing or in no sequence are zero
-        auto value = [&](auto careful, int r, float *f) {
+        auto value = [&](auto careful, int r, float (&f)[V]) {
             Pack<TV, V> x;
             if constexpr (M::ON) x = load<TV, V>(reinterpret_cast<const TV *>(pv + M::at_v(r)));
             else x = own_v[r];
-#pragma unroll
-            for (int j = 0; j < V; j++) f[j] = !decltype(careful)::value || in(r) ? to_f(x.v[j]) : 0.0f;
+            floats(f, x);
+            if (decltype(careful)::value && !in(r)) fill(f, 0.0f);
         };
-        auto gradient = [&](auto careful, int r, float *f) {
+        auto gradient = [&](auto careful, int r, float (&f)[V]) {
             Pack<TV, V> x;
             if constexpr (M::ON) x = load<TV, V>(reinterpret_cast<const TV *>(pd + M::at_v(r)));
             else x = own_d[r];
-#pragma unroll
-            for (int j = 0; j < V; j++) f[j] = !decltype(careful)::value || in(r) ? to_f(x.v[j]) : 0.0f;
+            floats(f, x);
+            if (decltype(careful)::value && !in(r)) fill(f, 0.0f);
+        };
+        auto opened = [&](int r, float (&a)[V], float (&c)[V]) {
+            float ka[GV], kc[GV];
+            open_gates<FORM>(k[r], ka, kc);
+            spread(a, ka);
+            spread(c, kc);
         };
 
         float P[V], Q[V], T[V], E[V];
         auto walk = [&](auto careful) {
             constexpr bool CARE = decltype(careful)::value;
-#pragma unroll
-            for (int j = 0; j < V; j++) P[j] = T[j] = 1.0f, Q[j] = E[j] = 0.0f;
+            fill(P, 1.0f);
+            fill(T, 1.0f);
+            fill(Q, 0.0f);
+            fill(E, 0.0f);
 #pragma unroll
             for (int r = 0; r < S::ROWS; r++) {
                 if (CARE && packed && edges) {
@@ -761,13 +907,16 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
 #pragma unroll
                         for (int j = 0; j < V; j++) P[j] = 0.0f, Q[j] = p.a.h0 ? p.a.h0[n * p.C + c + j] : 0.0f;
                 }
-                float v[V];
+                float v[V], a[V], b[V];
                 value(careful, r, v);
+                opened(r, a, b);
+                mul_all(P, P, a);
+                if constexpr (CARE) {
 #pragma unroll
-                for (int j = 0; j < V; j++) {
-                    const Gate q = open_gate<FORM>(k[r][HEAD ? 0 : j]);
-                    Q[j] = fma_if<CARE>(q.a, Q[j], FORM == GATED_SCAN_EXP ? v[j] : mul_if<CARE>(q.c, v[j]));
-                    P[j] *= q.a;
+                    for (int j = 0; j < V; j++) Q[j] = fma0(a[j], Q[j], FORM == GATED_SCAN_EXP ? v[j] : mul0(b[j], v[j]));
+                } else {
+                    if (FORM == GATED_SCAN_SIGMOID) mul_all(v, b, v);
+                    fma_all(Q, a, Q, v);
                 }
             }
 #pragma unroll
@@ -778,15 +927,20 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
 #pragma unroll
                         for (int j = 0; j < V; j++) T[j] = 0.0f, E[j] = p.a.dhT ? p.a.dhT[n * p.C + c + j] : 0.0f;
                 }
-                float d[V];
+                float d[V], a[V], b[V];
                 gradient(careful, r, d);
+                opened(r, a, b);
+                add_all(E, d, E);
+                if constexpr (CARE) {
 #pragma unroll
-                for (int j = 0; j < V; j++) {
-                    const float a = open_gate<FORM>(k[r][HEAD ? 0 : j]).a;
-                    E[j] = mul_if<CARE>(a, d[j] + E[j]);
-                    T[j] *= a;
+                    for (int j = 0; j < V; j++) E[j] = mul0(a[j], E[j]), T[j] *= a[j];
+                } else {
+                    mul_all(E, a, E);
                 }
             }
+            if (!CARE)
+#pragma unroll
+                for (int j = 0; j < V; j++) T[j] = P[j];   // the same product
         };
         bool fine = rows.count == S::ROWS && all_in && !edges;
         if (fine) {
@@ -816,10 +970,10 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
         __syncthreads();
 
         if (M::ON && agent) out_read();   // the other buffer's gradients have left it
-        fetch(ticket + gridDim.x, turn ^ 1);
-        fetch_gates(ticket + gridDim.x);
+        fetch(next, turn ^ 1);
+        fetch_gates(next);
         const int x = threadIdx.x, cx = c0 + threadIdx.x % S::WIDTH;
-        unsigned long long *const words = p.words + at.tile * S::WIDTH;
+        unsigned long long *const words = p.words + at.first_word(p) * S::WIDTH;
         const bool more = at.i + 1 < p.nchunk;
         float allT = 1.0f, allE = 0.0f;
         if (x < S::WIDTH) {
@@ -896,18 +1050,31 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
 #pragma unroll
                         for (int j = 0; j < V; j++) h[j] = p.a.h0 ? p.a.h0[n * p.C + c + j] : 0.0f;
                 }
-                float v[V];
+                float v[V], a[V], b[V];
                 value(careful, r, v);
+                opened(r, a, b);
+                if constexpr (CARE) {
 #pragma unroll
-                for (int j = 0; j < V; j++) {
-                    const Gate q = open_gate<FORM>(k[r][HEAD ? 0 : j]);
-                    slope[r][j] = FORM == GATED_SCAN_EXP ? mul_if<CARE>(q.a, h[j]) : mul_if<CARE>(q.a * q.c, h[j] - v[j]);
-                    h[j] = fma_if<CARE>(q.a, h[j], FORM == GATED_SCAN_EXP ? v[j] : mul_if<CARE>(q.c, v[j]));
+                    for (int j = 0; j < V; j++) {
+                        slope[r][j] = FORM == GATED_SCAN_EXP ? mul0(a[j], h[j]) : mul0(a[j] * b[j], h[j] - v[j]);
+                        h[j] = fma0(a[j], h[j], FORM == GATED_SCAN_EXP ? v[j] : mul0(b[j], v[j]));
+                    }
+                } else if constexpr (FORM == GATED_SCAN_EXP) {
+                    mul_all(slope[r], a, h);
+                    add_all(h, slope[r], v);
+                } else {
+                    float ah[V], less[V], minus[V];
+                    fill(minus, -1.0f);
+                    mul_all(ah, a, b);
+                    fma_all(less, v, minus, h);
+                    mul_all(slope[r], ah, less);
+                    mul_all(v, b, v);
+                    fma_all(h, a, h, v);
                 }
             }
             asm volatile("" ::: "memory");   // dv goes where the values were
             TV *dv_row = rows.template first<TV>(p.a.dv, c);
-            float head[HEAD ? S::ROWS : 1];
+            [[maybe_unused]] float head[HEAD ? S::ROWS : 1];
             TG *dg_row = rows.template first<TG>(p.a.dg, rows.gc);
 #pragma unroll
             for (int r = S::ROWS - 1; r >= 0; r--) {
@@ -918,15 +1085,26 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
 #pragma unroll
                         for (int j = 0; j < V; j++) e[j] = p.a.dhT ? p.a.dhT[n * p.C + c + j] : 0.0f;
                 }
-                float d[V], dv[V], dg[V];
+                float d[V], dv[V], dg[V], a[V], b[V];
                 gradient(careful, r, d);
+                opened(r, a, b);
+                add_all(d, d, e);
+                mul_all(dg, slope[r], d);
+                if constexpr (CARE) {
 #pragma unroll
-                for (int j = 0; j < V; j++) {
-                    const Gate q = open_gate<FORM>(k[r][HEAD ? 0 : j]);
-                    const float dh = d[j] + e[j];
-                    dg[j] = here ? slope[r][j] * dh : 0.0f;
-                    dv[j] = !here ? 0.0f : FORM == GATED_SCAN_EXP ? dh : mul_if<CARE>(q.c, dh);
-                    e[j] = mul_if<CARE>(q.a, dh);
+                    for (int j = 0; j < V; j++) {
+                        dv[j] = !here ? 0.0f : FORM == GATED_SCAN_EXP ? d[j] : mul0(b[j], d[j]);
+                        dg[j] = here ? dg[j] : 0.0f;
+                        e[j] = mul0(a[j], d[j]);
+                    }
+                } else {
+                    if (FORM == GATED_SCAN_EXP) {
+#pragma unroll
+                        for (int j = 0; j < V; j++) dv[j] = d[j];
+                    } else {
+                        mul_all(dv, b, d);
+                    }
+                    mul_all(e, a, d);
                 }
                 // rows of tiles that are not whole go straight to memory
                 const bool write = here || (r < rows.count && p.a.zero_outside);
@@ -1091,7 +1269,7 @@ struct Work {
 Work work_of(const gated_scan_s *h, long long B, long long L, bool backward, int V) {
     const size_t nchunk = (L + CHUNK - 1) / CHUNK;
     Work w{};
-    if (nchunk > 1) w.words = (size_t)B * strips_of(h, V) * nchunk * width_of(h, V) * 8;
+    if (nchunk > 1) w.words = ((size_t)B * strips_of(h, V) * nchunk + AHEAD) * width_of(h, V) * 8;
     w.words = (w.words + 255) / 256 * 256;
     const int pieces = backward ? pieces_of(h, V) : 1;
     if (pieces > 1) w.parts = (size_t)pieces * B * L * h->H * sizeof(float);
@@ -1173,7 +1351,7 @@ cudaError_t launch_tiles(Args &p, bool backward, const Work &w, cudaStream_t s) 
         if (!ok) return cudaErrorInvalidValue;
     }
     if (w.words) {
-        p.words = static_cast<unsigned long long *>(p.a.work);
+        p.words = static_cast<unsigned long long *>(p.a.work) + AHEAD * S::WIDTH;
         const cudaError_t e = cudaMemsetAsync(p.a.work, 0xff, w.words, s);
         if (e != cudaSuccess) return e;
     }
