@@ -260,6 +260,7 @@ constexpr unsigned MOST_POLLS = 1u << 22;   // of about a microsecond each
 struct Args {
     gated_scan_args a;
     int H, D, C;
+    unsigned long long head_of;   // ceil(2^40 / D): c * head_of >> 40 = c / D for c <= 2^20
     int strips;               // tiles beside one another: ceil(C / WIDTH)
     int nchunk;
     int nsm;
@@ -267,6 +268,8 @@ struct Args {
     unsigned long long *words;   // null where a sequence has one chunk
     float *parts;             // per-head gradients of heads that span strips: [pieces][B L][H]
 };
+
+__device__ __forceinline__ int head_of(const Args &p, int c) { return (int)((unsigned)c * p.head_of >> 40); }
 
 template <typename T> __device__ __forceinline__ T *row(const gated_scan_rows &r, long long b, long long t) {
     return static_cast<T *>(r.data) + b * r.batch_stride + t * r.row_stride;
@@ -296,23 +299,44 @@ __device__ __forceinline__ float word_Q(unsigned long long w) { return __uint_as
 
 // The state in front of tile i (counted in the direction of the walk) of a strip, for each of its
 // channels, found by the whole block: words[j * WIDTH + x] is tile j's word for channel x, and tile
-// 0's has P = 0.  Thread (q, x) asks for the REACH words at distances q * REACH + 1 and on, of
-// every q at once or, where the tiles in flight are few, of q = 0 first.  A channel is done when the
-// nearest word with P = 0 is among them and nothing is missing before it; tiles ahead that are not
-// done will be, so a block that finds no such word asks again instead of going further back.
+// 0's has P = 0.  Thread (q, x) asks for the REACH words at distances q * REACH + 1 and on.  A
+// channel is done when the nearest word with P = 0 is among them and nothing is missing before it;
+// tiles ahead that are not done will be, so a block that finds no such word asks again instead of
+// going further back.
 constexpr int REACH = 8;
 constexpr int AHEAD = 64;   // the most tiles that all threads of a block ask for
 template <int WIDTH, int QS> struct alignas(16) LookBack {
     float state[WIDTH];
     unsigned char seen[QS][WIDTH];
 };
+// The same for one channel by one thread, where few tiles are in flight.
+template <int WIDTH> __device__ __forceinline__ float look_near(const unsigned long long *words, int i) {
+    const unsigned long long *from = words + (long long)(i - 1) * WIDTH;
+    unsigned long long w[REACH];
+    for (unsigned polls = 0; polls < MOST_POLLS; polls++) {
+#pragma unroll
+        for (int j = 0; j < REACH; j++) w[j] = peek(from - j * WIDTH);
+        int seen = REACH;
+#pragma unroll
+        for (int j = REACH - 1; j >= 0; j--) {
+            const unsigned P = (unsigned)(w[j] >> 32);
+            seen = P == (unsigned)(NOTHING >> 32) ? REACH : P == 0 ? j : seen;
+        }
+        if (seen == REACH) continue;
+        float state = 0.0f;
+#pragma unroll
+        for (int j = REACH - 1; j >= 0; j--)
+            if (j <= seen) state = fma0(word_P(w[j]), state, word_Q(w[j]));
+        return state;
+    }
+    return __uint_as_float(0x7fc00000u);
+}
 template <int WIDTH, int QS>
-__device__ __forceinline__ void look_back(LookBack<WIDTH, QS> &m, const unsigned long long *words, int i, bool mine, bool far) {
+__device__ __forceinline__ void look_back(LookBack<WIDTH, QS> &m, const unsigned long long *words, int i, bool mine) {
     const int x = threadIdx.x % WIDTH, q = threadIdx.x / WIDTH;
     unsigned long long w[REACH];
     for (unsigned polls = 0;; polls++) {
-        const int qs = far || polls ? QS : 1;
-        if (q < qs) {
+        {
             // words ahead of tile 0 belong to others, or to nobody: tile 0's comes before them
             const unsigned long long *from = words + (long long)(i - 1 - q * REACH) * WIDTH + x;
 #pragma unroll
@@ -328,7 +352,7 @@ __device__ __forceinline__ void look_back(LookBack<WIDTH, QS> &m, const unsigned
         }
         __syncthreads();
         int from = 0, at = REACH;   // the word with P = 0: thread from's number at
-        while (from < qs && (at = m.seen[from][x]) == REACH) from++;
+        while (from < QS && (at = m.seen[from][x]) == REACH) from++;
         if (__syncthreads_or(at >= REACH)) {
             if (polls < MOST_POLLS) continue;
             if (q == 0) m.state[x] = __uint_as_float(0x7fc00000u);
@@ -336,13 +360,13 @@ __device__ __forceinline__ void look_back(LookBack<WIDTH, QS> &m, const unsigned
             return;
         }
         // from the farthest word on, in order
-        for (int k = __syncthreads_or(from > 0) ? qs - 1 : 0; k >= 0; k--) {
+        for (int k = __syncthreads_or(from > 0) ? QS - 1 : 0; k >= 0; k--) {
             if (q == k && k <= from) {
                 float state = k == from ? 0.0f : m.state[x];
 #pragma unroll
                 for (int j = REACH - 1; j >= 0; j--)
                     if (k < from || j <= at) state = fma0(word_P(w[j]), state, word_Q(w[j]));
-                m.state[x] = state;
+                m.state[x] = mine ? state : 0.0f;
             }
             __syncthreads();
         }
@@ -479,7 +503,7 @@ template <typename TV, typename TG, bool HEAD, int V> struct Rows {
         c0 = at.strip * S::WIDTH;
         c = c0 + threadIdx.x % S::LANES * V;
         mine = c < p.C;
-        gc = HEAD ? c / p.D : c;
+        gc = HEAD ? head_of(p, c) : c;
         t0 = (long long)chunk * CHUNK + threadIdx.x / S::LANES * S::ROWS;
         const long long left = p.a.L - t0;
         count = mine ? (int)(left < 0 ? 0 : left < S::ROWS ? left : S::ROWS) : 0;
@@ -487,18 +511,20 @@ template <typename TV, typename TG, bool HEAD, int V> struct Rows {
     template <typename T> __device__ T *first(const gated_scan_rows &r, int column) const { return row<T>(r, at.b, t0) + column; }
 };
 
-constexpr int FORWARD_BLOCKS = 2;   // of 256 threads an SM
+// Blocks an SM.
+template <typename TV, bool HEAD> constexpr int FORWARD_BLOCKS = HEAD && sizeof(TV) == 4 ? 5 : 3;
 
 template <typename TV, typename TG, int FORM, bool HEAD, int V>
-__global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / Tile<TV, V>::THREADS)
+__global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? 2 : FORWARD_BLOCKS<TV, HEAD>)
     scan_forward(const __grid_constant__ Args p, const __grid_constant__ Maps maps) {
     using S = Tile<TV, V>;
     using M = Stage<TV, TG, HEAD, V>;
     using R = Rows<TV, TG, HEAD, V>;
     constexpr int GV = HEAD ? 1 : V;
     constexpr bool FAST = sizeof(TV) == 2;
-    constexpr bool KEPT = M::ON && !HEAD;   // the gates' products are in shared memory, not in registers
+    constexpr bool KEPT = M::ON && !HEAD;   // the gates' products are where the gates were, not in registers
     extern __shared__ __align__(128) char buffers[];
+    __shared__ float head_P[HEAD && M::ON ? S::ROWS : 1][S::THREADS];   // a head's: one a row and thread
     __shared__ __align__(16) float sP[S::GROUPS][S::WIDTH], sQ[S::GROUPS][S::WIDTH];
     __shared__ LookBack<S::WIDTH, S::THREADS / S::WIDTH> ahead;
     __shared__ Marks marks;
@@ -526,8 +552,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / T
         const R rows(p, at, false);
         const TG *g = rows.template first<TG>(p.a.g, rows.gc);
 #pragma unroll
-        for (int r = 0; r < (HEAD ? S::ROWS : 1); r++)
-            if (r < rows.count) g_now[r] = g[r * p.a.g.row_stride];
+        for (int r = 0; r < (HEAD ? S::ROWS : 1); r++) g_now[r] = r < rows.count ? g[r * p.a.g.row_stride] : from_f<TG>(0.0f);
     };
     if (M::ON) {
         if (threadIdx.x == 0) {
@@ -556,10 +581,15 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / T
             starts = __syncthreads_or(f);
             ends = __syncthreads_or(l);
         }
-        const bool all_in = rows.t0 >= lo && rows.t0 + S::ROWS <= hi;
+        // every row that the tensors have is in a sequence, none starts one: rows and channels that
+        // do not exist come as zeros from the copies and go nowhere
+        const long long tile0 = (long long)at.i * CHUNK;
+        const bool whole = !packed || (tile0 >= lo && tile0 + CHUNK <= hi);
+        const bool plain = whole && !starts && (M::ON || (tile0 + CHUNK <= p.a.L && rows.mine));
 
         // row r's state is P[r] h + Q[r], h the state ahead of the thread's rows
-        float P[KEPT ? 1 : S::ROWS][GV], Q[S::ROWS][V], lastP[GV];
+        [[maybe_unused]] float P[M::ON ? 1 : S::ROWS][GV];
+        float Q[S::ROWS][V], lastP[GV];
         auto walk = [&](auto careful) {
             constexpr bool CARE = decltype(careful)::value;   // rows that are missing, starts, factors of zero
             float q[V];
@@ -620,6 +650,8 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / T
                 }
                 if constexpr (KEPT)
                     M::keep(pg, pv, r, lastP);
+                else if constexpr (M::ON)
+                    head_P[r][threadIdx.x] = lastP[0];
                 else
 #pragma unroll
                     for (int j = 0; j < GV; j++) P[r][j] = lastP[j];
@@ -631,7 +663,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / T
         if (M::ON) arrived = mbar_wait(smem_u32(&bars[turn]), phase, COPY_POLLS * 1000);
         // Without care a NaN or infinity anywhere leaves the last row without a finite value: then
         // the rows are walked again.
-        bool fine = rows.count == S::ROWS && all_in && !starts && arrived;
+        bool fine = plain && arrived;
         if (fine) {
             walk(std::false_type{});
 #pragma unroll
@@ -667,10 +699,13 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / T
                 allQ = fma0(gP, allQ, gQ);
                 allP *= gP;
             }
-            if (at.i > 0 && more && cx < p.C && allP != 0.0f) publish(words + (long long)at.i * S::WIDTH + x, allP, allQ);
+            if (at.i > 0 && more && cx < p.C) publish(words + (long long)at.i * S::WIDTH + x, allP, allQ);
         }
-        if (at.i > 0) {
-            look_back(ahead, words, at.i, cx < p.C, far);
+        if (at.i > 0 && far) {
+            look_back(ahead, words, at.i, cx < p.C);
+        } else if (at.i > 0) {
+            if (x < S::WIDTH) ahead.state[x] = cx < p.C ? look_near<S::WIDTH>(words + x, at.i) : 0.0f;
+            __syncthreads();
         } else {
             if (x < S::WIDTH) ahead.state[x] = !packed && p.a.h0 && cx < p.C ? p.a.h0[at.b * p.C + cx] : 0.0f;
             __syncthreads();
@@ -682,7 +717,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / T
         }
 
         float h0[V];
-        fine = rows.count == S::ROWS;
+        fine = plain && !ends;
         {
             float gp[V], gq[V], state[V];
             get(&sP[group][lane * V], gp);
@@ -694,8 +729,6 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / T
                 fine &= finite(h0[j]);
             }
         }
-        const long long tile0 = (long long)at.i * CHUNK;
-        const bool whole = !packed || (tile0 >= lo && tile0 + CHUNK <= hi);   // the tile's rows are all written, or do not exist
         auto finish = [&](auto careful) {
             constexpr bool CARE = decltype(careful)::value;
             TV *y = rows.template first<TV>(p.a.y, c);
@@ -704,6 +737,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / T
                 if (CARE && r >= rows.count) break;
                 float h[V], pr[V];
                 if constexpr (KEPT) M::kept(pg, pv, r, pr);
+                else if constexpr (M::ON) fill(pr, head_P[r][threadIdx.x]);
                 else spread(pr, P[r]);
                 if constexpr (CARE) {
 #pragma unroll
@@ -730,7 +764,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, FORWARD_BLOCKS * 256 / T
                 store<TV, V>(y + r * p.a.y.row_stride, h);
             }
         };
-        if (fine && whole && !ends)
+        if (fine)
             finish(std::false_type{});
         else
             finish(std::true_type{});
@@ -795,8 +829,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
         const R rows(p, at, true);
         const TG *g = rows.template first<TG>(p.a.g, rows.gc);
 #pragma unroll
-        for (int r = 0; r < (HEAD ? S::ROWS : 1); r++)
-            if (r < rows.count) g_now[r] = g[r * p.a.g.row_stride];
+        for (int r = 0; r < (HEAD ? S::ROWS : 1); r++) g_now[r] = r < rows.count ? g[r * p.a.g.row_stride] : from_f<TG>(0.0f);
     };
     if (M::ON) {
         if (threadIdx.x == 0) {
@@ -825,7 +858,8 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
             for (int i = threadIdx.x; i < CHUNK; i += S::THREADS) f |= marks.first[i] >= 0 || marks.last[i] >= 0;
             edges = __syncthreads_or(f);
         }
-        const bool all_in = rows.t0 >= lo && rows.t0 + S::ROWS <= hi;
+        const bool whole = !packed || (tile0 >= lo && tile0 + CHUNK <= hi);   // the tile's rows are all written, or do not exist
+        const bool plain = whole && !edges && tile0 + CHUNK <= p.a.L && (M::ON || rows.mine);
         auto in = [&](int r) { return r < rows.count && rows.t0 + r >= lo && rows.t0 + r < hi; };
         // the sequence that row r starts or ends, or -1
         auto starts = [&](int r) -> long long {
@@ -850,7 +884,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
 #pragma unroll
             for (int r = 0; r < S::ROWS; r++) {
                 Pack<TG, GV> g;
-                const bool there = in(r);
+                const bool there = plain || in(r);
                 if constexpr (M::ON) {
                     if constexpr (HEAD) g.v[0] = g_now[r];
                     else g = load<TG, GV>(reinterpret_cast<const TG *>(pg + M::at_g(r)));
@@ -867,7 +901,8 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
                 floats(gf, g);
                 pack_gates<FORM, FAST>(gf, k[r]);
 #pragma unroll
-                for (int j = 0; j < GV; j++) k[r][j] = there ? k[r][j] : HOLD<FORM>;
+                for (int j = 0; j < GV; j++)
+                    if (!there) k[r][j] = HOLD<FORM>;
             }
         }
         // row r of values or dy; rows that are missing or in no sequence are zero
@@ -942,7 +977,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
 #pragma unroll
                 for (int j = 0; j < V; j++) T[j] = P[j];   // the same product
         };
-        bool fine = rows.count == S::ROWS && all_in && !edges;
+        bool fine = plain;
         if (fine) {
             walk(std::false_type{});
 #pragma unroll
@@ -986,7 +1021,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
                 allE = fma0(gT, allE, gE);
                 allT *= gT;
             }
-            if (at.i > 0 && more && cx < p.C && allT != 0.0f) publish(words + (long long)at.i * S::WIDTH + x, allT, allE);
+            if (at.i > 0 && more && cx < p.C) publish(words + (long long)at.i * S::WIDTH + x, allT, allE);
         } else if (x < 2 * S::WIDTH) {
             // each group's result becomes the state ahead of it
             const int y = x - S::WIDTH;
@@ -1004,15 +1039,17 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
                 h = fma0(gP, h, gQ);
             }
         }
-        if (at.i > 0) {
-            look_back(ahead, words, at.i, cx < p.C, far);
+        if (at.i > 0 && far) {
+            look_back(ahead, words, at.i, cx < p.C);
+        } else if (at.i > 0) {
+            if (x < S::WIDTH) ahead.state[x] = cx < p.C ? look_near<S::WIDTH>(words + x, at.i) : 0.0f;
+            __syncthreads();
         } else {
             if (x < S::WIDTH) ahead.state[x] = 0.0f;
             __syncthreads();
         }
         if (x < S::WIDTH && cx < p.C && more) publish(words + (long long)at.i * S::WIDTH + x, 0.0f, fma0(allT, ahead.state[x], allE));
 
-        const bool whole = !packed || (tile0 >= lo && tile0 + CHUNK <= hi);   // the tile's rows are all written, or do not exist
         float h[V], e[V];
         {
             float gt[V], ge[V], grad[V];
@@ -1033,9 +1070,9 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
 #pragma unroll
             for (int o = 0; o < 5; o++) {
                 const int other = c + (V << o);
-                same[o] = lane + (1 << o) < S::LANES && other < p.C && other / p.D == rows.gc;
+                same[o] = lane + (1 << o) < S::LANES && other < p.C && head_of(p, other) == rows.gc;
             }
-            leader = rows.mine && (lane == 0 || (c - V) / p.D != rows.gc);
+            leader = rows.mine && (lane == 0 || head_of(p, c - V) != rows.gc);
         }
         const int piece = HEAD && rows.mine ? at.strip - first_strip(rows.gc, p.D, S::WIDTH) : 0;
         // forward again for the gate's slope at every row, then back with the gradient
@@ -1108,12 +1145,12 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
                 }
                 // rows of tiles that are not whole go straight to memory
                 const bool write = here || (r < rows.count && p.a.zero_outside);
-                if (M::ON && whole)
+                if (M::ON && (!CARE || whole))
                     store<TV, V>(reinterpret_cast<TV *>(pv + M::at_v(r)), dv);
                 else if (write)
                     store<TV, V>(dv_row + r * p.a.dv.row_stride, dv);
                 if constexpr (!HEAD) {
-                    if (M::ON && whole)
+                    if (M::ON && (!CARE || whole))
                         store<TG, V>(reinterpret_cast<TG *>(pg + M::at_g(r)), dg);
                     else if (write)
                         store<TG, V>(dg_row + r * p.a.dg.row_stride, dg);
@@ -1449,6 +1486,7 @@ int run(gated_scan_s *h, const gated_scan_args *a, bool backward, void *stream) 
     p.H = h->H;
     p.D = h->D;
     p.C = h->C;
+    p.head_of = ((1ull << 40) + h->D - 1) / h->D;
     p.strips = strips_of(h, V);
     p.nsm = h->nsm;
     p.nchunk = (int)nchunk;
