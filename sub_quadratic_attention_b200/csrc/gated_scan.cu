@@ -94,55 +94,6 @@ template <int FORM, bool FAST> __device__ __forceinline__ Gate gate_of(float g) 
     return g >= 0.0f ? Gate{o, s} : Gate{s, o};
 }
 
-// Two fp32 operations an instruction where a thread has channels in fours.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("{\n\t.reg .b64 a, b, c, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 r, a, b, c;\n\tmov.b64 {%0, %1}, r;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 r;
-    asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "mul.rn.f32x2 r, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 r;
-    asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "add.rn.f32x2 r, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-template <int V> __device__ __forceinline__ void fma_all(float (&r)[V], const float (&a)[V], const float (&b)[V], const float (&c)[V]) {
-    if constexpr (V == 4) {
-        const float2 x = fma2({a[0], a[1]}, {b[0], b[1]}, {c[0], c[1]}), y = fma2({a[2], a[3]}, {b[2], b[3]}, {c[2], c[3]});
-        r[0] = x.x, r[1] = x.y, r[2] = y.x, r[3] = y.y;
-    } else {
-        r[0] = fmaf(a[0], b[0], c[0]);
-    }
-}
-template <int V> __device__ __forceinline__ void mul_all(float (&r)[V], const float (&a)[V], const float (&b)[V]) {
-    if constexpr (V == 4) {
-        const float2 x = mul2({a[0], a[1]}, {b[0], b[1]}), y = mul2({a[2], a[3]}, {b[2], b[3]});
-        r[0] = x.x, r[1] = x.y, r[2] = y.x, r[3] = y.y;
-    } else {
-        r[0] = a[0] * b[0];
-    }
-}
-template <int V> __device__ __forceinline__ void add_all(float (&r)[V], const float (&a)[V], const float (&b)[V]) {
-    if constexpr (V == 4) {
-        const float2 x = add2({a[0], a[1]}, {b[0], b[1]}), y = add2({a[2], a[3]}, {b[2], b[3]});
-        r[0] = x.x, r[1] = x.y, r[2] = y.x, r[3] = y.y;
-    } else {
-        r[0] = a[0] + b[0];
-    }
-}
 template <int V> __device__ __forceinline__ void fill(float (&r)[V], float f) {
 #pragma unroll
     for (int j = 0; j < V; j++) r[j] = f;

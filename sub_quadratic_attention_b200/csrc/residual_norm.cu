@@ -1,9 +1,11 @@
 // residual_norm.cu -- y = N(out + x) or N(out) + x over rows of C values, N LayerNorm or
 // RMSNorm, its backward pass, and their C ABI (residual_norm.h).
 //
-// TPR threads (a power of two) hold one row in registers, at most 16 values a thread, so a
+// TPR threads (a power of two) hold one row in registers, EPT = 8 or 16 values a thread, so a
 // row is read once: the sums of a row are shuffles within a warp and, for rows wider than a
-// warp's share, one exchange of the warps' sums through shared memory.  The variance is
+// warp's share, one exchange of the warps' sums through shared memory.  A block walks over
+// rows and asks for the next row before it works on this one, so that a load's latency and
+// the sums' are not added up.  The variance is
 // taken about the mean in a second sum over the registers (a one-pass sum of squares loses
 // it where the mean is large).  The backward pass recomputes the row's statistics from its
 // registers instead of reading saved ones, and takes the three sums that need the mean (of
@@ -27,8 +29,8 @@ namespace resnorm {
 using namespace rows_io;
 
 constexpr int MAX_C = 8192;
-constexpr int EPT = 16;                    // values of a row that a thread holds
-constexpr int MAX_THREADS = MAX_C / EPT;   // 512
+constexpr int MAX_EPT = 16;                    // values of a row that a thread holds: 8 or 16
+constexpr int MAX_THREADS = MAX_C / MAX_EPT;   // 512
 constexpr int MIN_THREADS = 256;
 
 struct Args {
@@ -44,16 +46,31 @@ struct Args {
 };
 
 // VEC neighbouring values: one 16-byte access where VEC values are 16 bytes, else one value
-template <typename T, int VEC> struct Pack {
+template <typename T, int VEC> struct alignas(sizeof(T) * VEC) Pack {
     T v[VEC];
 };
+// Rows pass through once: they leave the first-level cache to gamma and beta.
 template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> load(const T *p) {
     Pack<T, VEC> r;
-    if constexpr (sizeof(T) * VEC == 16)
-        *reinterpret_cast<uint4 *>(r.v) = *reinterpret_cast<const uint4 *>(p);
-    else
-        r.v[0] = *p;
+    if constexpr (sizeof(T) * VEC == 16) {
+        uint4 u;
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+        *reinterpret_cast<uint4 *>(r.v) = u;
+    } else {
+        r.v[0] = __ldg(p);
+    }
     return r;
+}
+// VEC values of gamma or beta: from the first-level cache at every row, for registers are dearer
+template <int VEC> __device__ __forceinline__ void load_vector(float (&f)[VEC], const float *p) {
+    if constexpr (VEC >= 4) {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 4) {
+            asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f[j]), "=f"(f[j + 1]), "=f"(f[j + 2]), "=f"(f[j + 3]) : "l"(p + j));
+        }
+    } else {
+        f[0] = __ldg(p);
+    }
 }
 template <typename T, int VEC> __device__ __forceinline__ void store(T *p, const float *f) {
     Pack<T, VEC> r;
@@ -73,11 +90,11 @@ template <int K> __device__ __forceinline__ void row_sums(float (&s)[K], int tpr
         for (int k = 0; k < K; k++) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
     if (tpr <= 32) return;
     // two buffers in turn: a warp writes a buffer again only after the barrier that follows
-    // every warp's reads of it
+    // every warp's reads of it.  Each row of the block has a barrier of its own.
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
         for (int k = 0; k < K; k++) warp_sums[turn][k][threadIdx.x >> 5] = s[k];
-    __syncthreads();
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / tpr), "r"(tpr) : "memory");
 #pragma unroll
     for (int k = 0; k < K; k++) s[k] = 0.0f;
     const int first = threadIdx.x / tpr * (tpr / 32);   // the row's first warp
@@ -87,137 +104,199 @@ template <int K> __device__ __forceinline__ void row_sums(float (&s)[K], int tpr
     turn ^= 1;
 }
 
-template <typename T, int VEC, bool LN, bool POST>
-__global__ void __launch_bounds__(MAX_THREADS) norm_forward(Args a) {
+// A thread's part of a row of N tensors as it stands in memory.  Columns behind the last are
+// never asked for and stay zero; a row behind the last leaves what was there.
+template <typename T, int VEC, int EPT, int N> struct Part {
+    static constexpr int NV = EPT / VEC;
+    const T *at[N];        // the thread's first value of the row to ask for
+    long long step[N];     // to the block's next row
+    Pack<T, VEC> v[N][NV];
+    __device__ __forceinline__ void begin(int k, const void *p, long long stride, long long r, long long rows, int c) {
+        at[k] = static_cast<const T *>(p) + r * stride + c;
+        step[k] = rows * stride;
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+#pragma unroll
+            for (int j = 0; j < VEC; j++) v[k][i].v[j] = from_f<T>(0.0f);
+    }
+    __device__ __forceinline__ void fetch(bool there, const bool (&mine)[NV], int apart) {
+#pragma unroll
+        for (int k = 0; k < N; k++) {
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+                if (there && mine[i]) v[k][i] = load<T, VEC>(at[k] + i * apart);
+            at[k] += step[k];
+        }
+    }
+    __device__ __forceinline__ void floats(int k, int i, float (&f)[VEC]) const {
+#pragma unroll
+        for (int j = 0; j < VEC; j++) f[j] = to_f(v[k][i].v[j]);
+    }
+};
+// Registers a thread: what decides how many rows are in flight.
+template <int EPT, bool BACK> constexpr int REGISTERS = BACK ? (EPT == 8 ? 80 : 128) : (EPT == 8 ? 64 : 80);
+// The next row is asked for ahead where that costs at most 32 bytes a tensor and thread.
+template <typename T, int EPT> constexpr bool AHEAD = sizeof(T) * EPT <= 32;
+
+template <int N> __device__ __forceinline__ float sum_of(const float (&f)[N]) {
+    float s = f[0];
+#pragma unroll
+    for (int j = 1; j < N; j++) s += f[j];
+    return s;
+}
+
+template <typename T, int VEC, int EPT, bool LN, bool POST>
+__global__ void __maxnreg__((REGISTERS<EPT, false>)) norm_forward(const __grid_constant__ Args a) {
     constexpr int NV = EPT / VEC;
     const int lane = threadIdx.x % a.tpr, group = threadIdx.x / a.tpr, groups = blockDim.x / a.tpr;
+    const int c0 = lane * VEC, apart = a.tpr * VEC;
     const float inv = 1.0f / (float)a.C;
+    const long long rows = (long long)gridDim.x * groups;
+    long long r = blockIdx.x * (long long)groups + group;
+    bool mine[NV];
+#pragma unroll
+    for (int i = 0; i < NV; i++) mine[i] = c0 + i * apart < a.C;
     int turn = 0;
-    for (long long r0 = blockIdx.x * (long long)groups; r0 < a.T; r0 += (long long)gridDim.x * groups) {
-        const long long r = r0 + group;
-        const bool live = r < a.T;
-        float z[EPT], xr[POST ? 1 : EPT];
-        float s1[1] = {0.0f}, s2[1] = {0.0f};
+    Part<T, VEC, EPT, 2> next;
+    next.begin(0, a.out, a.outs, r, rows, c0);
+    next.begin(1, a.x, a.xs, r, rows, c0);
+    T *y = static_cast<T *>(a.y) + r * a.ys + c0;
+    if (AHEAD<T, EPT>) next.fetch(r < a.T, mine, apart);
+    for (long long r0 = blockIdx.x * (long long)groups; r0 < a.T; r0 += rows, r += rows, y += rows * a.ys) {
+        if (!AHEAD<T, EPT>) next.fetch(r < a.T, mine, apart);
+        float z[NV][VEC], sums[VEC], squares[VEC];
+        Pack<T, VEC> xr[POST ? 1 : NV];
+#pragma unroll
+        for (int j = 0; j < VEC; j++) sums[j] = squares[j] = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const int c = (i * a.tpr + lane) * VEC;
-            const bool in = live && c < a.C;
-            Pack<T, VEC> o, x;
-            if (in) {
-                o = load<T, VEC>(static_cast<const T *>(a.out) + r * a.outs + c);
-                x = load<T, VEC>(static_cast<const T *>(a.x) + r * a.xs + c);
+            next.floats(0, i, z[i]);
+            if constexpr (POST) {
+                float x[VEC];
+                next.floats(1, i, x);
+                add_all(z[i], z[i], x);
+            } else {
+                xr[i] = next.v[1][i];
             }
-#pragma unroll
-            for (int j = 0; j < VEC; j++) {
-                const float fo = in ? to_f(o.v[j]) : 0.0f, fx = in ? to_f(x.v[j]) : 0.0f;
-                z[i * VEC + j] = POST ? fo + fx : fo;
-                if constexpr (!POST) xr[i * VEC + j] = fx;
-                s1[0] += z[i * VEC + j];
-            }
+            if (LN) add_all(sums, sums, z[i]);
         }
-        float mean = 0.0f;
+        if (AHEAD<T, EPT>) next.fetch(r + rows < a.T, mine, apart);
+        float minus[VEC];
         if (LN) {
-            row_sums(s1, a.tpr, turn);
-            mean = s1[0] * inv;
+            float s[1] = {sum_of(sums)};
+            row_sums(s, a.tpr, turn);
+#pragma unroll
+            for (int j = 0; j < VEC; j++) minus[j] = -s[0] * inv;
         }
 #pragma unroll
         for (int i = 0; i < NV; i++)
-            if ((i * a.tpr + lane) * VEC < a.C)
+            if (mine[i]) {
+                if (LN) add_all(z[i], z[i], minus);
+                fma_all(squares, z[i], z[i], squares);
+            }
+        float s[1] = {sum_of(squares)};
+        row_sums(s, a.tpr, turn);
+        const float rstd = rsqrtf(s[0] * inv + a.eps);   // within two units of the last place
+        float scale[VEC];
 #pragma unroll
-                for (int j = 0; j < VEC; j++) {
-                    z[i * VEC + j] -= mean;
-                    s2[0] = fmaf(z[i * VEC + j], z[i * VEC + j], s2[0]);
-                }
-        row_sums(s2, a.tpr, turn);
-        const float rstd = 1.0f / sqrtf(s2[0] * inv + a.eps);
+        for (int j = 0; j < VEC; j++) scale[j] = rstd;
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const int c = (i * a.tpr + lane) * VEC;
-            if (!live || c >= a.C) continue;
-            float f[VEC];
+            if (r >= a.T || !mine[i]) continue;
+            float f[VEC], gamma[VEC], beta[VEC];
+            load_vector(gamma, a.gamma + c0 + i * apart);
+            load_vector(beta, a.beta + c0 + i * apart);
+            mul_all(f, z[i], scale);
+            fma_all(f, f, gamma, beta);
+            if constexpr (!POST)
 #pragma unroll
-            for (int j = 0; j < VEC; j++) {
-                f[j] = fmaf(z[i * VEC + j] * rstd, a.gamma[c + j], a.beta[c + j]);
-                if constexpr (!POST) f[j] += xr[i * VEC + j];
-            }
-            store<T, VEC>(static_cast<T *>(a.y) + r * a.ys + c, f);
+                for (int j = 0; j < VEC; j++) f[j] += to_f(xr[i].v[j]);
+            store<T, VEC>(y + i * apart, f);
         }
     }
 }
 
-template <typename T, int VEC, bool LN, bool POST>
-__global__ void __launch_bounds__(MAX_THREADS) norm_backward(Args a) {
+template <typename T, int VEC, int EPT, bool LN, bool POST>
+__global__ void __maxnreg__((REGISTERS<EPT, true>)) norm_backward(const __grid_constant__ Args a) {
     constexpr int NV = EPT / VEC;
     const int lane = threadIdx.x % a.tpr, group = threadIdx.x / a.tpr, groups = blockDim.x / a.tpr;
+    const int c0 = lane * VEC, apart = a.tpr * VEC;
     const float inv = 1.0f / (float)a.C;
+    const long long rows = (long long)gridDim.x * groups;
+    long long r = blockIdx.x * (long long)groups + group;
+    bool mine[NV];
+#pragma unroll
+    for (int i = 0; i < NV; i++) mine[i] = c0 + i * apart < a.C;
     int turn = 0;
-    float dgamma[EPT], dbeta[EPT];
+    float dgamma[NV][VEC], dbeta[NV][VEC];
 #pragma unroll
-    for (int i = 0; i < EPT; i++) dgamma[i] = dbeta[i] = 0.0f;
-    for (long long r0 = blockIdx.x * (long long)groups; r0 < a.T; r0 += (long long)gridDim.x * groups) {
-        const long long r = r0 + group;
-        const bool live = r < a.T;
-        float z[EPT], dy[EPT];
-        float s1[1] = {0.0f}, s[3] = {0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < EPT; i++) dgamma[i / VEC][i % VEC] = dbeta[i / VEC][i % VEC] = 0.0f;
+    Part<T, VEC, EPT, POST ? 3 : 2> next;
+    next.begin(0, a.out, a.outs, r, rows, c0);
+    next.begin(1, a.dy, a.dys, r, rows, c0);
+    if constexpr (POST) next.begin(2, a.x, a.xs, r, rows, c0);
+    T *dz = static_cast<T *>(a.y) + r * a.ys + c0;
+    if (AHEAD<T, EPT>) next.fetch(r < a.T, mine, apart);
+    for (long long r0 = blockIdx.x * (long long)groups; r0 < a.T; r0 += rows, r += rows, dz += rows * a.ys) {
+        if (!AHEAD<T, EPT>) next.fetch(r < a.T, mine, apart);
+        float z[NV][VEC], dy[NV][VEC], sums[VEC], squares[VEC], along[VEC], level[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; j++) sums[j] = squares[j] = along[j] = level[j] = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const int c = (i * a.tpr + lane) * VEC;
-            const bool in = live && c < a.C;
-            Pack<T, VEC> o, x, d;
-            if (in) {
-                o = load<T, VEC>(static_cast<const T *>(a.out) + r * a.outs + c);
-                if constexpr (POST) x = load<T, VEC>(static_cast<const T *>(a.x) + r * a.xs + c);
-                d = load<T, VEC>(static_cast<const T *>(a.dy) + r * a.dys + c);
+            next.floats(0, i, z[i]);
+            next.floats(1, i, dy[i]);
+            if constexpr (POST) {
+                float x[VEC];
+                next.floats(2, i, x);
+                add_all(z[i], z[i], x);
             }
-#pragma unroll
-            for (int j = 0; j < VEC; j++) {
-                const int e = i * VEC + j;
-                z[e] = in ? to_f(o.v[j]) : 0.0f;
-                if constexpr (POST) z[e] += in ? to_f(x.v[j]) : 0.0f;
-                dy[e] = in ? to_f(d.v[j]) : 0.0f;
-                s1[0] += z[e];
-            }
+            if (LN) add_all(sums, sums, z[i]);
         }
-        float mean = 0.0f;
+        if (AHEAD<T, EPT>) next.fetch(r + rows < a.T, mine, apart);
+        float minus[VEC];
         if (LN) {
-            row_sums(s1, a.tpr, turn);
-            mean = s1[0] * inv;
+            float s[1] = {sum_of(sums)};
+            row_sums(s, a.tpr, turn);
+#pragma unroll
+            for (int j = 0; j < VEC; j++) minus[j] = -s[0] * inv;
         }
 #pragma unroll
-        for (int i = 0; i < NV; i++) {
-            const int c = (i * a.tpr + lane) * VEC;
-            if (c >= a.C) continue;
-#pragma unroll
-            for (int j = 0; j < VEC; j++) {
-                const int e = i * VEC + j;
-                const float dn = dy[e] * a.gamma[c + j];
-                z[e] -= mean;
-                s[0] = fmaf(z[e], z[e], s[0]);
-                s[1] = fmaf(dn, z[e], s[1]);
-                s[2] += dn;
+        for (int i = 0; i < NV; i++)
+            if (mine[i]) {
+                float dn[VEC];
+                load_vector(dn, a.gamma + c0 + i * apart);
+                mul_all(dn, dn, dy[i]);
+                if (LN) {
+                    add_all(z[i], z[i], minus);
+                    add_all(level, level, dn);
+                }
+                fma_all(squares, z[i], z[i], squares);
+                fma_all(along, dn, z[i], along);
             }
-        }
+        float s[3] = {sum_of(squares), sum_of(along), LN ? sum_of(level) : 0.0f};
         row_sums(s, a.tpr, turn);
-        const float rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
-        const float along = s[1] * rstd * inv, level = LN ? s[2] * inv : 0.0f;
+        const float rstd = rsqrtf(s[0] * inv + a.eps);   // within two units of the last place
+        float scale[VEC], toward[VEC], off[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; j++) scale[j] = rstd, toward[j] = -s[1] * rstd * inv, off[j] = -s[2] * inv;
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const int c = (i * a.tpr + lane) * VEC;
-            if (!live || c >= a.C) continue;
+            if (r >= a.T || !mine[i]) continue;
             float f[VEC];
-#pragma unroll
-            for (int j = 0; j < VEC; j++) {
-                const int e = i * VEC + j;
-                const float n = z[e] * rstd;
-                dgamma[e] = fmaf(dy[e], n, dgamma[e]);
-                dbeta[e] += dy[e];
-                f[j] = rstd * (fmaf(-n, along, dy[e] * a.gamma[c + j]) - level);
-            }
-            store<T, VEC>(static_cast<T *>(a.y) + r * a.ys + c, f);
+            load_vector(f, a.gamma + c0 + i * apart);
+            mul_all(z[i], z[i], scale);
+            add_all(dbeta[i], dbeta[i], dy[i]);
+            fma_all(dgamma[i], dy[i], z[i], dgamma[i]);
+            if (LN) fma_all(f, f, dy[i], off);
+            else mul_all(f, f, dy[i]);
+            fma_all(f, z[i], toward, f);
+            mul_all(f, f, scale);
+            store<T, VEC>(dz + i * apart, f);
         }
     }
     // the block's row groups add their columns in turn
-    __shared__ float sums[2][MIN_THREADS * EPT / 2];
+    __shared__ float all[2][MIN_THREADS * EPT / 2];   // two row groups at least: half of the block's columns
     float *pg = a.part_gamma + blockIdx.x * a.part_stride, *pb = a.part_beta + blockIdx.x * a.part_stride;
     for (int g = 0; g < groups; g++) {
         if (group == g)
@@ -225,18 +304,18 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_backward(Args a) {
             for (int i = 0; i < NV; i++)
 #pragma unroll
                 for (int j = 0; j < VEC; j++) {
-                    const int c = (i * a.tpr + lane) * VEC + j, e = i * VEC + j;
-                    if (c >= a.C) continue;
+                    const int c = c0 + i * apart + j;
+                    if (!mine[i]) continue;
                     if (g) {
-                        dgamma[e] += sums[0][c];
-                        dbeta[e] += sums[1][c];
+                        dgamma[i][j] += all[0][c];
+                        dbeta[i][j] += all[1][c];
                     }
                     if (g == groups - 1) {
-                        pg[c] = dgamma[e];
-                        pb[c] = dbeta[e];
+                        pg[c] = dgamma[i][j];
+                        pb[c] = dbeta[i][j];
                     } else {
-                        sums[0][c] = dgamma[e];
-                        sums[1][c] = dbeta[e];
+                        all[0][c] = dgamma[i][j];
+                        all[1][c] = dbeta[i][j];
                     }
                 }
         if (groups > 1) __syncthreads();
@@ -258,27 +337,46 @@ __global__ void __launch_bounds__(JOIN_COLS *JOIN_ROWS) join_blocks(const float 
     (c < C ? dgamma[c] : dbeta[c - C]) = s;
 }
 
-// The row's threads: the fewest that hold it with EPT values each, and four at least; a block
-// has the rows that fill MIN_THREADS.
-int threads_per_row(int C) {
+// The row's threads and the values of each, 8 or 16; the fewest threads that hold the row, and four
+// at least.  A block has the rows that fill MIN_THREADS.
+int values_per_thread(int C, int dtype, bool backward) {
+    if (C <= 32 * 8) return 8;
+    if (backward) return C <= MIN_THREADS * 8 ? 8 : 16;
+    return dtype == SPECTRE_F32 && C <= MAX_THREADS * 8 ? 8 : 16;
+}
+int threads_per_row(int C, int dtype, bool backward) {
     int tpr = 4;
-    while (tpr * EPT < C) tpr *= 2;
+    while (tpr * values_per_thread(C, dtype, backward) < C) tpr *= 2;
     return tpr;
 }
 int block_threads(int tpr) { return tpr > MIN_THREADS ? tpr : MIN_THREADS; }
 
-constexpr int BLOCKS_PER_SM = 2;
+// Blocks that run at once.
+long long resident_blocks(const residual_norm_s *h, bool backward) {
+    const bool eight = values_per_thread(h->C, h->dtype, backward) == 8;
+    const int registers = backward ? (eight ? REGISTERS<8, true> : REGISTERS<16, true>) : (eight ? REGISTERS<8, false> : REGISTERS<16, false>);
+    const int threads = block_threads(threads_per_row(h->C, h->dtype, backward)), n = 65536 / registers / threads;
+    return (long long)h->nsm * (n > 0 ? n : 1);
+}
 long long backward_blocks(const residual_norm_s *h, long long T) {
-    const int tpr = threads_per_row(h->C), groups = block_threads(tpr) / tpr;
-    const long long need = (T + groups - 1) / groups, most = (long long)h->nsm * BLOCKS_PER_SM;
+    const int tpr = threads_per_row(h->C, h->dtype, true), groups = block_threads(tpr) / tpr;
+    const long long need = (T + groups - 1) / groups, most = resident_blocks(h, true);
     return need < most ? need : most;
 }
 
 template <typename T, int VEC, bool LN, bool POST> void launch(const Args &a, bool backward, int grid, cudaStream_t s) {
-    if (backward)
-        norm_backward<T, VEC, LN, POST><<<grid, block_threads(a.tpr), 0, s>>>(a);
-    else
-        norm_forward<T, VEC, LN, POST><<<grid, block_threads(a.tpr), 0, s>>>(a);
+    const int threads = block_threads(a.tpr);
+    if (values_per_thread(a.C, sizeof(T) == 4 ? SPECTRE_F32 : SPECTRE_BF16, backward) == 8) {
+        if (backward)
+            norm_backward<T, VEC, 8, LN, POST><<<grid, threads, 0, s>>>(a);
+        else
+            norm_forward<T, VEC, 8, LN, POST><<<grid, threads, 0, s>>>(a);
+    } else {
+        if (backward)
+            norm_backward<T, VEC, 16, LN, POST><<<grid, threads, 0, s>>>(a);
+        else
+            norm_forward<T, VEC, 16, LN, POST><<<grid, threads, 0, s>>>(a);
+    }
 }
 
 template <typename T, int VEC> void launch_norm(int norm, const Args &a, bool backward, int grid, cudaStream_t s) {
@@ -295,7 +393,7 @@ bool wide(const void *p, long long stride, size_t es) { return aligned(p, 16) &&
 int enqueue(const residual_norm_s *h, Args &a, bool backward, int grid, cudaStream_t s) {
     const size_t es = h->dtype == SPECTRE_F32 ? 4 : 2;
     const bool vec = (h->C * es) % 16 == 0 && wide(a.out, a.outs, es) && wide(a.x, a.xs, es) && wide(a.y, a.ys, es) &&
-                     wide(a.dy, a.dys, es);
+                     wide(a.dy, a.dys, es) && aligned(a.gamma, 16) && aligned(a.beta, 16);
     if (h->dtype == SPECTRE_F32)
         vec ? launch_norm<float, 4>(h->norm, a, backward, grid, s) : launch_norm<float, 1>(h->norm, a, backward, grid, s);
     else
@@ -343,7 +441,7 @@ int residual_norm_run(residual_norm_t h, long long T, const void *out, long long
     Args a{};
     a.T = T;
     a.C = h->C;
-    a.tpr = threads_per_row(h->C);
+    a.tpr = threads_per_row(h->C, h->dtype, false);
     a.eps = h->eps;
     a.out = out;
     a.outs = out_stride;
@@ -354,7 +452,7 @@ int residual_norm_run(residual_norm_t h, long long T, const void *out, long long
     a.gamma = gamma;
     a.beta = beta;
     const int groups = block_threads(a.tpr) / a.tpr;
-    const long long need = (T + groups - 1) / groups, most = (long long)h->nsm * 8;
+    const long long need = (T + groups - 1) / groups, most = resident_blocks(h, false);
     return enqueue(h, a, false, (int)(need < most ? need : most), static_cast<cudaStream_t>(stream));
 }
 
@@ -388,7 +486,7 @@ int residual_norm_backward(residual_norm_t h, long long T, const void *dy, long 
         Args a{};
         a.T = T;
         a.C = h->C;
-        a.tpr = threads_per_row(h->C);
+        a.tpr = threads_per_row(h->C, h->dtype, true);
         a.eps = h->eps;
         a.dy = dy;
         a.dys = dy_stride;
