@@ -3,9 +3,10 @@
 //
 // TPR threads (a power of two) hold one row in registers, EPT = 8 or 16 values a thread, so a
 // row is read once: the sums of a row are shuffles within a warp and, for rows wider than a
-// warp's share, one exchange of the warps' sums through shared memory.  A block walks over
-// rows and asks for the next row before it works on this one, so that a load's latency and
-// the sums' are not added up.  The variance is
+// warp's share, one exchange of the warps' sums through shared memory.  Rows come by bulk
+// copies into a ring of stages that each row's threads have for themselves, so that the next
+// rows are on their way without a register while this one is worked on; rows that cannot be
+// copied so (short, or not 16-byte aligned) are loaded by the threads.  The variance is
 // taken about the mean in a second sum over the registers (a one-pass sum of squares loses
 // it where the mean is large).  The backward pass recomputes the row's statistics from its
 // registers instead of reading saved ones, and takes the three sums that need the mean (of
@@ -17,6 +18,7 @@
 
 #include "residual_norm.h"
 #include "rows_io.cuh"
+#include "tc_dft.cuh"
 
 struct residual_norm_s {
     int C, dtype, norm;
@@ -43,7 +45,13 @@ struct Args {
     const float *gamma, *beta;
     float *part_gamma, *part_beta;   // backward: block i's sums at + i * part_stride
     long long part_stride;
+    int stages, stage_bytes;   // of the ring
 };
+
+constexpr int MAX_STAGES = 4;
+constexpr int MAX_RINGS = MIN_THREADS / 32;   // rows of a block that have one: a warp's or wider
+constexpr uint32_t COPY_POLLS = 4000;         // of up to a millisecond's suspension each
+
 
 // VEC neighbouring values: one 16-byte access where VEC values are 16 bytes, else one value
 template <typename T, int VEC> struct alignas(sizeof(T) * VEC) Pack {
@@ -85,10 +93,20 @@ template <typename T, int VEC> __device__ __forceinline__ void store(T *p, const
 // K sums over the row's threads, in every one of them; the same order for every row
 template <int K> __device__ __forceinline__ void row_sums(float (&s)[K], int tpr, int &turn) {
     __shared__ float warp_sums[2][K][MAX_THREADS / 32];
-    for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1)
+    if (tpr >= 32) {
 #pragma unroll
-        for (int k = 0; k < K; k++) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
-    if (tpr <= 32) return;
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < K; k++) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+    } else {
+        for (int o = tpr >> 1; o > 0; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < K; k++) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+    }
+    if (tpr <= 32) {
+        __syncwarp();
+        return;
+    }
     // two buffers in turn: a warp writes a buffer again only after the barrier that follows
     // every warp's reads of it.  Each row of the block has a barrier of its own.
     if ((threadIdx.x & 31) == 0)
@@ -97,35 +115,93 @@ template <int K> __device__ __forceinline__ void row_sums(float (&s)[K], int tpr
     asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / tpr), "r"(tpr) : "memory");
 #pragma unroll
     for (int k = 0; k < K; k++) s[k] = 0.0f;
-    const int first = threadIdx.x / tpr * (tpr / 32);   // the row's first warp
-    for (int w = first; w < first + tpr / 32; w++)
+    const int first = threadIdx.x / tpr * (tpr / 32), warps = tpr / 32;   // the row's warps: up to 16
 #pragma unroll
-        for (int k = 0; k < K; k++) s[k] += warp_sums[turn][k][w];
+    for (int k = 0; k < K; k++) s[k] = warp_sums[turn][k][first + (threadIdx.x & (warps - 1))];
+    for (int o = warps >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < K; k++) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
     turn ^= 1;
 }
 
-// A thread's part of a row of N tensors as it stands in memory.  Columns behind the last are
-// never asked for and stay zero; a row behind the last leaves what was there.
-template <typename T, int VEC, int EPT, int N> struct Part {
+using spectre::tc::bulk_copy_g2s;
+using spectre::tc::mbar_arrive_expect_tx;
+using spectre::tc::mbar_init;
+using spectre::tc::mbar_wait;
+using spectre::tc::smem_u32;
+
+// A thread's part of a row of N tensors as it stands in memory; columns and rows that do not
+// exist are zero.
+template <typename T, int VEC, int EPT, int N, bool RING> struct Part {
     static constexpr int NV = EPT / VEC;
-    const T *at[N];        // the thread's first value of the row to ask for
+    const T *at[N];        // the row to ask for: its first value, or the thread's
     long long step[N];     // to the block's next row
     Pack<T, VEC> v[N][NV];
+    char *ring;
+    uint32_t bars;
+    int stages, stage_bytes, stage, bytes;
+    uint32_t phase;
+    bool leader;
     __device__ __forceinline__ void begin(int k, const void *p, long long stride, long long r, long long rows, int c) {
-        at[k] = static_cast<const T *>(p) + r * stride + c;
+        at[k] = static_cast<const T *>(p) + r * stride + (RING ? 0 : c);
         step[k] = rows * stride;
-#pragma unroll
-        for (int i = 0; i < NV; i++)
-#pragma unroll
-            for (int j = 0; j < VEC; j++) v[k][i].v[j] = from_f<T>(0.0f);
     }
-    __device__ __forceinline__ void fetch(bool there, const bool (&mine)[NV], int apart) {
+    // the rows' rings, and the first rows on their way
+    __device__ __forceinline__ void open(const Args &a, char *buffers, unsigned long long *all, int group, int lane, long long r, long long rows) {
+        stages = a.stages;
+        if constexpr (RING) {
+            stage_bytes = a.stage_bytes;
+            bytes = a.C * (int)sizeof(T);
+            ring = buffers + group * stages * stage_bytes;
+            bars = smem_u32(all + group * MAX_STAGES);
+            stage = 0;
+            phase = 0;
+            leader = lane == 0;
+            if (leader)
+                for (int i = 0; i < stages; i++) mbar_init(bars + 8 * i, 1);
+            __syncthreads();
+            for (int i = 0; i < stages; i++) {
+                send(i, r < a.T);
+                r += rows;
+            }
+        }
+    }
+    __device__ __forceinline__ void send(int s, bool there) {
+        if (there && leader) {
+            mbar_arrive_expect_tx(bars + 8 * s, N * bytes);
+#pragma unroll
+            for (int k = 0; k < N; k++) bulk_copy_g2s(smem_u32(ring + s * stage_bytes) + k * bytes, at[k], bytes, bars + 8 * s);
+        }
+#pragma unroll
+        for (int k = 0; k < N; k++) at[k] += step[k];
+    }
+    // the row's values, or false where they did not come
+    __device__ __forceinline__ bool fetch(bool there, const bool (&mine)[NV], int c, int apart) {
+        bool came = true;
+        if (RING && there) came = mbar_wait(bars + 8 * stage, phase, COPY_POLLS);
 #pragma unroll
         for (int k = 0; k < N; k++) {
 #pragma unroll
-            for (int i = 0; i < NV; i++)
-                if (there && mine[i]) v[k][i] = load<T, VEC>(at[k] + i * apart);
-            at[k] += step[k];
+            for (int i = 0; i < NV; i++) {
+                if (!there || !mine[i]) {
+#pragma unroll
+                    for (int j = 0; j < VEC; j++) v[k][i].v[j] = from_f<T>(0.0f);
+                    continue;
+                }
+                if constexpr (RING)
+                    v[k][i] = *reinterpret_cast<const Pack<T, VEC> *>(ring + stage * stage_bytes + k * bytes + (c + i * apart) * (int)sizeof(T));
+                else
+                    v[k][i] = load<T, VEC>(at[k] + i * apart);
+            }
+            if (!RING) at[k] += step[k];
+        }
+        return came;
+    }
+    // after every thread of the row has its values: the stage's next row
+    __device__ __forceinline__ void pass(bool there) {
+        if constexpr (RING) {
+            send(stage, there);
+            if (++stage == stages) stage = 0, phase ^= 1;
         }
     }
     __device__ __forceinline__ void floats(int k, int i, float (&f)[VEC]) const {
@@ -135,8 +211,8 @@ template <typename T, int VEC, int EPT, int N> struct Part {
 };
 // Registers a thread: what decides how many rows are in flight.
 template <int EPT, bool BACK> constexpr int REGISTERS = BACK ? (EPT == 8 ? 80 : 128) : (EPT == 8 ? 64 : 80);
-// The next row is asked for ahead where that costs at most 32 bytes a tensor and thread.
-template <typename T, int EPT> constexpr bool AHEAD = sizeof(T) * EPT <= 32;
+// The next row is loaded ahead where it has no ring and costs at most 32 bytes a tensor and thread.
+template <typename T, int EPT, bool RING> constexpr bool AHEAD = !RING && sizeof(T) * EPT <= 32;
 
 template <int N> __device__ __forceinline__ float sum_of(const float (&f)[N]) {
     float s = f[0];
@@ -145,8 +221,10 @@ template <int N> __device__ __forceinline__ float sum_of(const float (&f)[N]) {
     return s;
 }
 
-template <typename T, int VEC, int EPT, bool LN, bool POST>
+template <typename T, int VEC, int EPT, bool RING, bool LN, bool POST>
 __global__ void __maxnreg__((REGISTERS<EPT, false>)) norm_forward(const __grid_constant__ Args a) {
+    extern __shared__ __align__(128) char buffers[];
+    __shared__ __align__(8) unsigned long long bars[RING ? MAX_RINGS * MAX_STAGES : 1];
     constexpr int NV = EPT / VEC;
     const int lane = threadIdx.x % a.tpr, group = threadIdx.x / a.tpr, groups = blockDim.x / a.tpr;
     const int c0 = lane * VEC, apart = a.tpr * VEC;
@@ -157,13 +235,16 @@ __global__ void __maxnreg__((REGISTERS<EPT, false>)) norm_forward(const __grid_c
 #pragma unroll
     for (int i = 0; i < NV; i++) mine[i] = c0 + i * apart < a.C;
     int turn = 0;
-    Part<T, VEC, EPT, 2> next;
+    Part<T, VEC, EPT, 2, RING> next;
     next.begin(0, a.out, a.outs, r, rows, c0);
     next.begin(1, a.x, a.xs, r, rows, c0);
     T *y = static_cast<T *>(a.y) + r * a.ys + c0;
-    if (AHEAD<T, EPT>) next.fetch(r < a.T, mine, apart);
+    next.open(a, buffers, bars, group, lane, r, rows);
+    constexpr bool EARLY = AHEAD<T, EPT, RING>;
+    if (EARLY) next.fetch(r < a.T, mine, c0, apart);
     for (long long r0 = blockIdx.x * (long long)groups; r0 < a.T; r0 += rows, r += rows, y += rows * a.ys) {
-        if (!AHEAD<T, EPT>) next.fetch(r < a.T, mine, apart);
+        bool came = true;
+        if (!EARLY) came = next.fetch(r < a.T, mine, c0, apart);
         float z[NV][VEC], sums[VEC], squares[VEC];
         Pack<T, VEC> xr[POST ? 1 : NV];
 #pragma unroll
@@ -180,7 +261,7 @@ __global__ void __maxnreg__((REGISTERS<EPT, false>)) norm_forward(const __grid_c
             }
             if (LN) add_all(sums, sums, z[i]);
         }
-        if (AHEAD<T, EPT>) next.fetch(r + rows < a.T, mine, apart);
+        if (EARLY) next.fetch(r + rows < a.T, mine, c0, apart);
         float minus[VEC];
         if (LN) {
             float s[1] = {sum_of(sums)};
@@ -196,7 +277,8 @@ __global__ void __maxnreg__((REGISTERS<EPT, false>)) norm_forward(const __grid_c
             }
         float s[1] = {sum_of(squares)};
         row_sums(s, a.tpr, turn);
-        const float rstd = rsqrtf(s[0] * inv + a.eps);   // within two units of the last place
+        next.pass(r + next.stages * rows < a.T);
+        const float rstd = came ? rsqrtf(s[0] * inv + a.eps) : __uint_as_float(0x7fc00000u);   // within two units of the last place
         float scale[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; j++) scale[j] = rstd;
@@ -216,8 +298,10 @@ __global__ void __maxnreg__((REGISTERS<EPT, false>)) norm_forward(const __grid_c
     }
 }
 
-template <typename T, int VEC, int EPT, bool LN, bool POST>
+template <typename T, int VEC, int EPT, bool RING, bool LN, bool POST>
 __global__ void __maxnreg__((REGISTERS<EPT, true>)) norm_backward(const __grid_constant__ Args a) {
+    extern __shared__ __align__(128) char buffers[];
+    __shared__ __align__(8) unsigned long long bars[RING ? MAX_RINGS * MAX_STAGES : 1];
     constexpr int NV = EPT / VEC;
     const int lane = threadIdx.x % a.tpr, group = threadIdx.x / a.tpr, groups = blockDim.x / a.tpr;
     const int c0 = lane * VEC, apart = a.tpr * VEC;
@@ -231,14 +315,17 @@ __global__ void __maxnreg__((REGISTERS<EPT, true>)) norm_backward(const __grid_c
     float dgamma[NV][VEC], dbeta[NV][VEC];
 #pragma unroll
     for (int i = 0; i < EPT; i++) dgamma[i / VEC][i % VEC] = dbeta[i / VEC][i % VEC] = 0.0f;
-    Part<T, VEC, EPT, POST ? 3 : 2> next;
+    Part<T, VEC, EPT, POST ? 3 : 2, RING> next;
     next.begin(0, a.out, a.outs, r, rows, c0);
     next.begin(1, a.dy, a.dys, r, rows, c0);
     if constexpr (POST) next.begin(2, a.x, a.xs, r, rows, c0);
     T *dz = static_cast<T *>(a.y) + r * a.ys + c0;
-    if (AHEAD<T, EPT>) next.fetch(r < a.T, mine, apart);
+    next.open(a, buffers, bars, group, lane, r, rows);
+    constexpr bool EARLY = AHEAD<T, EPT, RING>;
+    if (EARLY) next.fetch(r < a.T, mine, c0, apart);
     for (long long r0 = blockIdx.x * (long long)groups; r0 < a.T; r0 += rows, r += rows, dz += rows * a.ys) {
-        if (!AHEAD<T, EPT>) next.fetch(r < a.T, mine, apart);
+        bool came = true;
+        if (!EARLY) came = next.fetch(r < a.T, mine, c0, apart);
         float z[NV][VEC], dy[NV][VEC], sums[VEC], squares[VEC], along[VEC], level[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; j++) sums[j] = squares[j] = along[j] = level[j] = 0.0f;
@@ -253,7 +340,7 @@ __global__ void __maxnreg__((REGISTERS<EPT, true>)) norm_backward(const __grid_c
             }
             if (LN) add_all(sums, sums, z[i]);
         }
-        if (AHEAD<T, EPT>) next.fetch(r + rows < a.T, mine, apart);
+        if (EARLY) next.fetch(r + rows < a.T, mine, c0, apart);
         float minus[VEC];
         if (LN) {
             float s[1] = {sum_of(sums)};
@@ -276,7 +363,8 @@ __global__ void __maxnreg__((REGISTERS<EPT, true>)) norm_backward(const __grid_c
             }
         float s[3] = {sum_of(squares), sum_of(along), LN ? sum_of(level) : 0.0f};
         row_sums(s, a.tpr, turn);
-        const float rstd = rsqrtf(s[0] * inv + a.eps);   // within two units of the last place
+        next.pass(r + next.stages * rows < a.T);
+        const float rstd = came ? rsqrtf(s[0] * inv + a.eps) : __uint_as_float(0x7fc00000u);   // within two units of the last place
         float scale[VEC], toward[VEC], off[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; j++) scale[j] = rstd, toward[j] = -s[1] * rstd * inv, off[j] = -s[2] * inv;
@@ -364,22 +452,27 @@ long long backward_blocks(const residual_norm_s *h, long long T) {
     return need < most ? need : most;
 }
 
-template <typename T, int VEC, bool LN, bool POST> void launch(const Args &a, bool backward, int grid, cudaStream_t s) {
-    const int threads = block_threads(a.tpr);
-    if (values_per_thread(a.C, sizeof(T) == 4 ? SPECTRE_F32 : SPECTRE_BF16, backward) == 8) {
-        if (backward)
-            norm_backward<T, VEC, 8, LN, POST><<<grid, threads, 0, s>>>(a);
-        else
-            norm_forward<T, VEC, 8, LN, POST><<<grid, threads, 0, s>>>(a);
-    } else {
-        if (backward)
-            norm_backward<T, VEC, 16, LN, POST><<<grid, threads, 0, s>>>(a);
-        else
-            norm_forward<T, VEC, 16, LN, POST><<<grid, threads, 0, s>>>(a);
+template <typename T, int VEC, int EPT, bool RING, bool LN, bool POST>
+cudaError_t launch_rows(const Args &a, bool backward, int grid, cudaStream_t s) {
+    const int threads = block_threads(a.tpr), bytes = RING ? threads / a.tpr * a.stages * a.stage_bytes : 0;
+    const auto kernel = backward ? norm_backward<T, VEC, EPT, RING, LN, POST> : norm_forward<T, VEC, EPT, RING, LN, POST>;
+    if (RING) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
     }
+    kernel<<<grid, threads, bytes, s>>>(a);
+    return cudaGetLastError();
 }
 
-template <typename T, int VEC> void launch_norm(int norm, const Args &a, bool backward, int grid, cudaStream_t s) {
+template <typename T, int VEC, bool LN, bool POST> cudaError_t launch(const Args &a, bool backward, int grid, cudaStream_t s) {
+    const bool eight = values_per_thread(a.C, sizeof(T) == 4 ? SPECTRE_F32 : SPECTRE_BF16, backward) == 8;
+    if constexpr (VEC > 1)
+        if (a.stages)
+            return eight ? launch_rows<T, VEC, 8, true, LN, POST>(a, backward, grid, s) : launch_rows<T, VEC, 16, true, LN, POST>(a, backward, grid, s);
+    return eight ? launch_rows<T, VEC, 8, false, LN, POST>(a, backward, grid, s) : launch_rows<T, VEC, 16, false, LN, POST>(a, backward, grid, s);
+}
+
+template <typename T, int VEC> cudaError_t launch_norm(int norm, const Args &a, bool backward, int grid, cudaStream_t s) {
     switch (norm) {
     case SPECTRE_NORM_POST_LN: return launch<T, VEC, true, true>(a, backward, grid, s);
     case SPECTRE_NORM_PRE_LN: return launch<T, VEC, true, false>(a, backward, grid, s);
@@ -388,18 +481,30 @@ template <typename T, int VEC> void launch_norm(int norm, const Args &a, bool ba
     }
 }
 
+// An SM's shared memory for the blocks on it, and what a block needs beside its rings.
+constexpr int SM_SHARED_BYTES = 227 * 1024, BLOCK_SHARED_BYTES = 20 * 1024;
+
 bool wide(const void *p, long long stride, size_t es) { return aligned(p, 16) && (stride * es) % 16 == 0; }
 
 int enqueue(const residual_norm_s *h, Args &a, bool backward, int grid, cudaStream_t s) {
     const size_t es = h->dtype == SPECTRE_F32 ? 4 : 2;
     const bool vec = (h->C * es) % 16 == 0 && wide(a.out, a.outs, es) && wide(a.x, a.xs, es) && wide(a.y, a.ys, es) &&
                      wide(a.dy, a.dys, es) && aligned(a.gamma, 16) && aligned(a.beta, 16);
+    // rings: rows of a warp or more, each stage one row of every input; four stages where they fit
+    a.stages = 0;
+    if (vec && a.tpr >= 32) {
+        const int inputs = backward ? (a.x ? 3 : 2) : 2, rings = block_threads(a.tpr) / a.tpr;
+        a.stage_bytes = inputs * a.C * (int)es;
+        const int blocks = (int)(resident_blocks(h, backward) / h->nsm), room = (SM_SHARED_BYTES / blocks - BLOCK_SHARED_BYTES) / rings / a.stage_bytes;
+        a.stages = room < MAX_STAGES ? room : MAX_STAGES;
+        if (a.stages < 2) a.stages = 0;
+    }
+    cudaError_t e;
     if (h->dtype == SPECTRE_F32)
-        vec ? launch_norm<float, 4>(h->norm, a, backward, grid, s) : launch_norm<float, 1>(h->norm, a, backward, grid, s);
+        e = vec ? launch_norm<float, 4>(h->norm, a, backward, grid, s) : launch_norm<float, 1>(h->norm, a, backward, grid, s);
     else
-        vec ? launch_norm<__nv_bfloat16, 8>(h->norm, a, backward, grid, s)
-            : launch_norm<__nv_bfloat16, 1>(h->norm, a, backward, grid, s);
-    return status_of(cudaGetLastError());
+        e = vec ? launch_norm<__nv_bfloat16, 8>(h->norm, a, backward, grid, s) : launch_norm<__nv_bfloat16, 1>(h->norm, a, backward, grid, s);
+    return status_of(e);
 }
 
 size_t partial_bytes(const residual_norm_s *h, long long T) {
