@@ -47,9 +47,6 @@ using namespace rows_io;
 
 constexpr int CHUNK = GATED_SCAN_CHUNK;
 
-template <typename T, int V> struct alignas(sizeof(T) * V) Pack {
-    T v[V];
-};
 template <typename T, int V> __device__ __forceinline__ Pack<T, V> load(const T *p) {
     return *reinterpret_cast<const Pack<T, V> *>(p);
 }
@@ -92,6 +89,56 @@ template <int FORM, bool FAST> __device__ __forceinline__ Gate gate_of(float g) 
     if (FORM == GATED_SCAN_EXP) return {expf(g), 1.0f};
     const float s = smaller_factor<FAST>(g), o = 1.0f - s;
     return g >= 0.0f ? Gate{o, s} : Gate{s, o};
+}
+
+// Two fp32 operations an instruction, on neighbouring values of a thread.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 r, a, b, c;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 r, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 r, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+template <int N> __device__ __forceinline__ void fma_all(float (&r)[N], const float (&a)[N], const float (&b)[N], const float (&c)[N]) {
+#pragma unroll
+    for (int j = 0; j + 1 < N; j += 2) {
+        const float2 x = fma2({a[j], a[j + 1]}, {b[j], b[j + 1]}, {c[j], c[j + 1]});
+        r[j] = x.x, r[j + 1] = x.y;
+    }
+    if constexpr (N % 2) r[N - 1] = fmaf(a[N - 1], b[N - 1], c[N - 1]);
+}
+template <int N> __device__ __forceinline__ void mul_all(float (&r)[N], const float (&a)[N], const float (&b)[N]) {
+#pragma unroll
+    for (int j = 0; j + 1 < N; j += 2) {
+        const float2 x = mul2({a[j], a[j + 1]}, {b[j], b[j + 1]});
+        r[j] = x.x, r[j + 1] = x.y;
+    }
+    if constexpr (N % 2) r[N - 1] = a[N - 1] * b[N - 1];
+}
+template <int N> __device__ __forceinline__ void add_all(float (&r)[N], const float (&a)[N], const float (&b)[N]) {
+#pragma unroll
+    for (int j = 0; j + 1 < N; j += 2) {
+        const float2 x = add2({a[j], a[j + 1]}, {b[j], b[j + 1]});
+        r[j] = x.x, r[j + 1] = x.y;
+    }
+    if constexpr (N % 2) r[N - 1] = a[N - 1] + b[N - 1];
 }
 
 template <int V> __device__ __forceinline__ void fill(float (&r)[V], float f) {

@@ -53,10 +53,7 @@ constexpr int MAX_RINGS = MIN_THREADS / 32;   // rows of a block that have one: 
 constexpr uint32_t COPY_POLLS = 4000;         // of up to a millisecond's suspension each
 
 
-// VEC neighbouring values: one 16-byte access where VEC values are 16 bytes, else one value
-template <typename T, int VEC> struct alignas(sizeof(T) * VEC) Pack {
-    T v[VEC];
-};
+// VEC neighbouring values: one 16-byte access where they are 16 bytes, else one value.
 // Rows pass through once: they leave the first-level cache to gamma and beta.
 template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> load(const T *p) {
     Pack<T, VEC> r;
@@ -69,25 +66,20 @@ template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> load(cons
     }
     return r;
 }
-// VEC values of gamma or beta: from the first-level cache at every row, for registers are dearer
-template <int VEC> __device__ __forceinline__ void load_vector(float (&f)[VEC], const float *p) {
-    if constexpr (VEC >= 4) {
-#pragma unroll
-        for (int j = 0; j < VEC; j += 4) {
-            asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f[j]), "=f"(f[j + 1]), "=f"(f[j + 2]), "=f"(f[j + 3]) : "l"(p + j));
-        }
+// VEC values of gamma or beta: from the first-level cache at every row, for registers are dearer.
+template <int VEC> __device__ __forceinline__ Vec<VEC> load_vector(const float *p) {
+    Vec<VEC> r;
+    if constexpr (VEC == 1) {
+        r.p = __ldg(p);
     } else {
-        f[0] = __ldg(p);
-    }
-}
-template <typename T, int VEC> __device__ __forceinline__ void store(T *p, const float *f) {
-    Pack<T, VEC> r;
 #pragma unroll
-    for (int j = 0; j < VEC; j++) r.v[j] = from_f<T>(f[j]);
-    if constexpr (sizeof(T) * VEC == 16)
-        *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<uint4 *>(r.v);
-    else
-        *p = r.v[0];
+        for (int i = 0; i < VEC / 2; i += 2)
+            asm volatile("ld.global.nc.v2.u64 {%0, %1}, [%2];" : "=l"(r.p[i]), "=l"(r.p[i + 1]) : "l"(p + 2 * i));
+    }
+    return r;
+}
+template <typename T, int VEC> __device__ __forceinline__ void store(T *p, const Vec<VEC> &f) {
+    *reinterpret_cast<Pack<T, VEC> *>(p) = packed<T, VEC>(f);
 }
 
 // K sums over the row's threads, in every one of them; the same order for every row
@@ -204,22 +196,11 @@ template <typename T, int VEC, int EPT, int N, bool RING> struct Part {
             if (++stage == stages) stage = 0, phase ^= 1;
         }
     }
-    __device__ __forceinline__ void floats(int k, int i, float (&f)[VEC]) const {
-#pragma unroll
-        for (int j = 0; j < VEC; j++) f[j] = to_f(v[k][i].v[j]);
-    }
 };
 // Registers a thread: what decides how many rows are in flight.
 template <int EPT, bool BACK> constexpr int REGISTERS = BACK ? (EPT == 8 ? 80 : 128) : (EPT == 8 ? 64 : 80);
 // The next row is loaded ahead where it has no ring and costs at most 32 bytes a tensor and thread.
 template <typename T, int EPT, bool RING> constexpr bool AHEAD = !RING && sizeof(T) * EPT <= 32;
-
-template <int N> __device__ __forceinline__ float sum_of(const float (&f)[N]) {
-    float s = f[0];
-#pragma unroll
-    for (int j = 1; j < N; j++) s += f[j];
-    return s;
-}
 
 template <typename T, int VEC, int EPT, bool RING, bool LN, bool POST>
 __global__ void __maxnreg__((REGISTERS<EPT, false>)) norm_forward(const __grid_constant__ Args a) {
@@ -245,54 +226,38 @@ __global__ void __maxnreg__((REGISTERS<EPT, false>)) norm_forward(const __grid_c
     for (long long r0 = blockIdx.x * (long long)groups; r0 < a.T; r0 += rows, r += rows, y += rows * a.ys) {
         bool came = true;
         if (!EARLY) came = next.fetch(r < a.T, mine, c0, apart);
-        float z[NV][VEC], sums[VEC], squares[VEC];
+        Vec<VEC> z[NV], sums(0.0f), squares(0.0f);
         Pack<T, VEC> xr[POST ? 1 : NV];
 #pragma unroll
-        for (int j = 0; j < VEC; j++) sums[j] = squares[j] = 0.0f;
-#pragma unroll
         for (int i = 0; i < NV; i++) {
-            next.floats(0, i, z[i]);
-            if constexpr (POST) {
-                float x[VEC];
-                next.floats(1, i, x);
-                add_all(z[i], z[i], x);
-            } else {
-                xr[i] = next.v[1][i];
-            }
-            if (LN) add_all(sums, sums, z[i]);
+            z[i] = floats(next.v[0][i]);
+            if constexpr (POST) z[i] = z[i] + floats(next.v[1][i]);
+            else xr[i] = next.v[1][i];
+            if (LN) sums = sums + z[i];
         }
         if (EARLY) next.fetch(r + rows < a.T, mine, c0, apart);
-        float minus[VEC];
+        Vec<VEC> minus(0.0f);
         if (LN) {
             float s[1] = {sum_of(sums)};
             row_sums(s, a.tpr, turn);
-#pragma unroll
-            for (int j = 0; j < VEC; j++) minus[j] = -s[0] * inv;
+            minus = Vec<VEC>(-s[0] * inv);
         }
 #pragma unroll
         for (int i = 0; i < NV; i++)
             if (mine[i]) {
-                if (LN) add_all(z[i], z[i], minus);
-                fma_all(squares, z[i], z[i], squares);
+                if (LN) z[i] = z[i] + minus;
+                squares = fma(z[i], z[i], squares);
             }
         float s[1] = {sum_of(squares)};
         row_sums(s, a.tpr, turn);
         next.pass(r + next.stages * rows < a.T);
         const float rstd = came ? rsqrtf(s[0] * inv + a.eps) : __uint_as_float(0x7fc00000u);   // within two units of the last place
-        float scale[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; j++) scale[j] = rstd;
+        const Vec<VEC> scale(rstd);
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             if (r >= a.T || !mine[i]) continue;
-            float f[VEC], gamma[VEC], beta[VEC];
-            load_vector(gamma, a.gamma + c0 + i * apart);
-            load_vector(beta, a.beta + c0 + i * apart);
-            mul_all(f, z[i], scale);
-            fma_all(f, f, gamma, beta);
-            if constexpr (!POST)
-#pragma unroll
-                for (int j = 0; j < VEC; j++) f[j] += to_f(xr[i].v[j]);
+            Vec<VEC> f = fma(z[i] * scale, load_vector<VEC>(a.gamma + c0 + i * apart), load_vector<VEC>(a.beta + c0 + i * apart));
+            if constexpr (!POST) f = f + floats(xr[i]);
             store<T, VEC>(y + i * apart, f);
         }
     }
@@ -312,9 +277,9 @@ __global__ void __maxnreg__((REGISTERS<EPT, true>)) norm_backward(const __grid_c
 #pragma unroll
     for (int i = 0; i < NV; i++) mine[i] = c0 + i * apart < a.C;
     int turn = 0;
-    float dgamma[NV][VEC], dbeta[NV][VEC];
+    Vec<VEC> dgamma[NV], dbeta[NV];
 #pragma unroll
-    for (int i = 0; i < EPT; i++) dgamma[i / VEC][i % VEC] = dbeta[i / VEC][i % VEC] = 0.0f;
+    for (int i = 0; i < NV; i++) dgamma[i] = dbeta[i] = Vec<VEC>(0.0f);
     Part<T, VEC, EPT, POST ? 3 : 2, RING> next;
     next.begin(0, a.out, a.outs, r, rows, c0);
     next.begin(1, a.dy, a.dys, r, rows, c0);
@@ -326,61 +291,46 @@ __global__ void __maxnreg__((REGISTERS<EPT, true>)) norm_backward(const __grid_c
     for (long long r0 = blockIdx.x * (long long)groups; r0 < a.T; r0 += rows, r += rows, dz += rows * a.ys) {
         bool came = true;
         if (!EARLY) came = next.fetch(r < a.T, mine, c0, apart);
-        float z[NV][VEC], dy[NV][VEC], sums[VEC], squares[VEC], along[VEC], level[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; j++) sums[j] = squares[j] = along[j] = level[j] = 0.0f;
+        Vec<VEC> z[NV], dy[NV], sums(0.0f), squares(0.0f), along(0.0f), level(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            next.floats(0, i, z[i]);
-            next.floats(1, i, dy[i]);
-            if constexpr (POST) {
-                float x[VEC];
-                next.floats(2, i, x);
-                add_all(z[i], z[i], x);
-            }
-            if (LN) add_all(sums, sums, z[i]);
+            z[i] = floats(next.v[0][i]);
+            dy[i] = floats(next.v[1][i]);
+            if constexpr (POST) z[i] = z[i] + floats(next.v[2][i]);
+            if (LN) sums = sums + z[i];
         }
         if (EARLY) next.fetch(r + rows < a.T, mine, c0, apart);
-        float minus[VEC];
+        Vec<VEC> minus(0.0f);
         if (LN) {
             float s[1] = {sum_of(sums)};
             row_sums(s, a.tpr, turn);
-#pragma unroll
-            for (int j = 0; j < VEC; j++) minus[j] = -s[0] * inv;
+            minus = Vec<VEC>(-s[0] * inv);
         }
 #pragma unroll
         for (int i = 0; i < NV; i++)
             if (mine[i]) {
-                float dn[VEC];
-                load_vector(dn, a.gamma + c0 + i * apart);
-                mul_all(dn, dn, dy[i]);
+                const Vec<VEC> dn = dy[i] * load_vector<VEC>(a.gamma + c0 + i * apart);
                 if (LN) {
-                    add_all(z[i], z[i], minus);
-                    add_all(level, level, dn);
+                    z[i] = z[i] + minus;
+                    level = level + dn;
                 }
-                fma_all(squares, z[i], z[i], squares);
-                fma_all(along, dn, z[i], along);
+                squares = fma(z[i], z[i], squares);
+                along = fma(dn, z[i], along);
             }
         float s[3] = {sum_of(squares), sum_of(along), LN ? sum_of(level) : 0.0f};
         row_sums(s, a.tpr, turn);
         next.pass(r + next.stages * rows < a.T);
         const float rstd = came ? rsqrtf(s[0] * inv + a.eps) : __uint_as_float(0x7fc00000u);   // within two units of the last place
-        float scale[VEC], toward[VEC], off[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; j++) scale[j] = rstd, toward[j] = -s[1] * rstd * inv, off[j] = -s[2] * inv;
+        // r (dn - mean(dn) - n mean(dn n)), the means' factors taken together
+        const Vec<VEC> scale(rstd), toward(-s[1] * rstd * inv * rstd), off(-s[2] * inv * rstd);
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             if (r >= a.T || !mine[i]) continue;
-            float f[VEC];
-            load_vector(f, a.gamma + c0 + i * apart);
-            mul_all(z[i], z[i], scale);
-            add_all(dbeta[i], dbeta[i], dy[i]);
-            fma_all(dgamma[i], dy[i], z[i], dgamma[i]);
-            if (LN) fma_all(f, f, dy[i], off);
-            else mul_all(f, f, dy[i]);
-            fma_all(f, z[i], toward, f);
-            mul_all(f, f, scale);
-            store<T, VEC>(dz + i * apart, f);
+            const Vec<VEC> n = z[i] * scale, dn = dy[i] * load_vector<VEC>(a.gamma + c0 + i * apart);
+            dbeta[i] = dbeta[i] + dy[i];
+            dgamma[i] = fma(dy[i], n, dgamma[i]);
+            const Vec<VEC> less = LN ? fma(n, toward, off) : n * toward;
+            store<T, VEC>(dz + i * apart, fma(dn, scale, less));
         }
     }
     // the block's row groups add their columns in turn
@@ -395,8 +345,8 @@ __global__ void __maxnreg__((REGISTERS<EPT, true>)) norm_backward(const __grid_c
                     const int c = c0 + i * apart + j;
                     if (!mine[i]) continue;
                     if (g) {
-                        dgamma[i][j] += all[0][c];
-                        dbeta[i][j] += all[1][c];
+                        dgamma[i].set(j, dgamma[i][j] + all[0][c]);
+                        dbeta[i].set(j, dbeta[i][j] + all[1][c]);
                     }
                     if (g == groups - 1) {
                         pg[c] = dgamma[i][j];
@@ -429,7 +379,7 @@ __global__ void __launch_bounds__(JOIN_COLS *JOIN_ROWS) join_blocks(const float 
 // at least.  A block has the rows that fill MIN_THREADS.
 int values_per_thread(int C, int dtype, bool backward) {
     if (C <= 32 * 8) return 8;
-    if (backward) return C <= MIN_THREADS * 8 ? 8 : 16;
+    if (backward) return 16;
     return dtype == SPECTRE_F32 && C <= MAX_THREADS * 8 ? 8 : 16;
 }
 int threads_per_row(int C, int dtype, bool backward) {

@@ -19,54 +19,109 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float
     return __float2bfloat16_rn(v);
 }
 
-// Two fp32 operations an instruction, on neighbouring values of a thread.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("{\n\t.reg .b64 a, b, c, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 r, a, b, c;\n\tmov.b64 {%0, %1}, r;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+// N neighbouring fp32 values of a thread, in pairs on which one instruction does two operations
+// (N even), or one value.  The pairs stay 64-bit registers from operation to operation.
+__device__ __forceinline__ unsigned long long pair_of(float x, float y) {
+    unsigned long long p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    return p;
+}
+template <int N> struct Vec {
+    static_assert(N % 2 == 0, "");
+    unsigned long long p[N / 2];
+    __device__ __forceinline__ Vec() {}
+    __device__ __forceinline__ explicit Vec(float f) {
+#pragma unroll
+        for (int i = 0; i < N / 2; i++) p[i] = pair_of(f, f);
+    }
+    __device__ __forceinline__ float operator[](int j) const {
+        float x, y;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p[j / 2]));
+        return j % 2 ? y : x;
+    }
+    __device__ __forceinline__ void set(int j, float f) { p[j / 2] = j % 2 ? pair_of((*this)[j - 1], f) : pair_of(f, (*this)[j + 1]); }
+};
+template <> struct Vec<1> {
+    float p;
+    __device__ __forceinline__ Vec() {}
+    __device__ __forceinline__ explicit Vec(float f) : p(f) {}
+    __device__ __forceinline__ float operator[](int) const { return p; }
+    __device__ __forceinline__ void set(int, float f) { p = f; }
+};
+template <int N> __device__ __forceinline__ Vec<N> operator+(const Vec<N> &a, const Vec<N> &b) {
+    Vec<N> r;
+    if constexpr (N == 1) r.p = a.p + b.p;
+    else
+#pragma unroll
+        for (int i = 0; i < N / 2; i++) asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.p[i]) : "l"(a.p[i]), "l"(b.p[i]));
     return r;
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 r;
-    asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "mul.rn.f32x2 r, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+template <int N> __device__ __forceinline__ Vec<N> operator*(const Vec<N> &a, const Vec<N> &b) {
+    Vec<N> r;
+    if constexpr (N == 1) r.p = a.p * b.p;
+    else
+#pragma unroll
+        for (int i = 0; i < N / 2; i++) asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.p[i]) : "l"(a.p[i]), "l"(b.p[i]));
     return r;
 }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 r;
-    asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "add.rn.f32x2 r, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+template <int N> __device__ __forceinline__ Vec<N> fma(const Vec<N> &a, const Vec<N> &b, const Vec<N> &c) {
+    Vec<N> r;
+    if constexpr (N == 1) r.p = fmaf(a.p, b.p, c.p);
+    else
+#pragma unroll
+        for (int i = 0; i < N / 2; i++) asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.p[i]) : "l"(a.p[i]), "l"(b.p[i]), "l"(c.p[i]));
     return r;
 }
-template <int N> __device__ __forceinline__ void fma_all(float (&r)[N], const float (&a)[N], const float (&b)[N], const float (&c)[N]) {
+template <int N> __device__ __forceinline__ float sum_of(Vec<N> v) {
+    if constexpr (N == 1) {
+        return v.p;
+    } else if constexpr (N == 2) {
+        return v[0] + v[1];
+    } else {
+        Vec<N / 2> a, b;
 #pragma unroll
-    for (int j = 0; j + 1 < N; j += 2) {
-        const float2 x = fma2({a[j], a[j + 1]}, {b[j], b[j + 1]}, {c[j], c[j + 1]});
-        r[j] = x.x, r[j + 1] = x.y;
+        for (int i = 0; i < N / 4; i++) a.p[i] = v.p[i], b.p[i] = v.p[i + N / 4];
+        return sum_of(a + b);
     }
-    if constexpr (N % 2) r[N - 1] = fmaf(a[N - 1], b[N - 1], c[N - 1]);
 }
-template <int N> __device__ __forceinline__ void mul_all(float (&r)[N], const float (&a)[N], const float (&b)[N]) {
+
+// N values as they stand in memory, aligned to all of them.
+template <typename T, int N> struct alignas(sizeof(T) * N) Pack {
+    T v[N];
+};
+template <int N> __device__ __forceinline__ Vec<N> floats(const Pack<float, N> &x) {
+    Vec<N> r;
+    if constexpr (N == 1) r.p = x.v[0];
+    else
 #pragma unroll
-    for (int j = 0; j + 1 < N; j += 2) {
-        const float2 x = mul2({a[j], a[j + 1]}, {b[j], b[j + 1]});
-        r[j] = x.x, r[j + 1] = x.y;
-    }
-    if constexpr (N % 2) r[N - 1] = a[N - 1] * b[N - 1];
+        for (int i = 0; i < N / 2; i++) r.p[i] = pair_of(x.v[2 * i], x.v[2 * i + 1]);
+    return r;
 }
-template <int N> __device__ __forceinline__ void add_all(float (&r)[N], const float (&a)[N], const float (&b)[N]) {
+template <int N> __device__ __forceinline__ Vec<N> floats(const Pack<__nv_bfloat16, N> &x) {
+    Vec<N> r;
+    if constexpr (N == 1) r.p = __bfloat162float(x.v[0]);
+    else
 #pragma unroll
-    for (int j = 0; j + 1 < N; j += 2) {
-        const float2 x = add2({a[j], a[j + 1]}, {b[j], b[j + 1]});
-        r[j] = x.x, r[j + 1] = x.y;
+        for (int i = 0; i < N / 2; i++) {
+            const unsigned u = reinterpret_cast<const unsigned *>(x.v)[i];   // a bf16 is a float's upper half
+            r.p[i] = pair_of(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+        }
+    return r;
+}
+template <typename T, int N> __device__ __forceinline__ Pack<T, N> packed(const Vec<N> &f) {
+    Pack<T, N> r;
+    if constexpr (N > 1 && sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < N / 2; i++) {
+            unsigned u;
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+            reinterpret_cast<unsigned *>(r.v)[i] = u;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; j++) r.v[j] = from_f<T>(f[j]);
     }
-    if constexpr (N % 2) r[N - 1] = a[N - 1] + b[N - 1];
+    return r;
 }
 
 inline bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
