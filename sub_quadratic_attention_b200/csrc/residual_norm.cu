@@ -107,12 +107,16 @@ template <int K> __device__ __forceinline__ void row_sums(float (&s)[K], int tpr
     asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / tpr), "r"(tpr) : "memory");
 #pragma unroll
     for (int k = 0; k < K; k++) s[k] = 0.0f;
-    const int first = threadIdx.x / tpr * (tpr / 32), warps = tpr / 32;   // the row's warps: up to 16
+    // the row's warps, 2 to 16, taken as 16: each of them counts 16 / warps times, which a power of
+    // two takes back exactly
+    const int first = threadIdx.x / tpr * (tpr / 32), warps = tpr / 32;
+    const float share = (float)warps * 0.0625f;
 #pragma unroll
-    for (int k = 0; k < K; k++) s[k] = warp_sums[turn][k][first + (threadIdx.x & (warps - 1))];
-    for (int o = warps >> 1; o > 0; o >>= 1)
+    for (int k = 0; k < K; k++) {
+        s[k] = warp_sums[turn][k][first + (threadIdx.x & (warps - 1))] * share;
 #pragma unroll
-        for (int k = 0; k < K; k++) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+        for (int o = 8; o > 0; o >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+    }
     turn ^= 1;
 }
 
@@ -168,7 +172,7 @@ template <typename T, int VEC, int EPT, int N, bool RING> struct Part {
         for (int k = 0; k < N; k++) at[k] += step[k];
     }
     // the row's values, or false where they did not come
-    __device__ __forceinline__ bool fetch(bool there, const bool (&mine)[NV], int c, int apart) {
+    template <typename M> __device__ __forceinline__ bool fetch(bool there, const M &mine, int c, int apart) {
         bool came = true;
         if (RING && there) came = mbar_wait(bars + 8 * stage, phase, COPY_POLLS);
 #pragma unroll
@@ -197,12 +201,23 @@ template <typename T, int VEC, int EPT, int N, bool RING> struct Part {
         }
     }
 };
+// Which of a thread's values exist: all of them where the threads' shares fill the row.
+template <int NV, bool FULL> struct Mine {
+    bool m[FULL ? 1 : NV];
+    __device__ __forceinline__ Mine(int c, int apart, int C) {
+        if (!FULL)
+#pragma unroll
+            for (int i = 0; i < NV; i++) m[FULL ? 0 : i] = c + i * apart < C;
+    }
+    __device__ __forceinline__ bool operator[](int i) const { return FULL || m[FULL ? 0 : i]; }
+};
+
 // Registers a thread: what decides how many rows are in flight.
 template <int EPT, bool BACK> constexpr int REGISTERS = BACK ? (EPT == 8 ? 80 : 128) : (EPT == 8 ? 64 : 80);
 // The next row is loaded ahead where it has no ring and costs at most 32 bytes a tensor and thread.
 template <typename T, int EPT, bool RING> constexpr bool AHEAD = !RING && sizeof(T) * EPT <= 32;
 
-template <typename T, int VEC, int EPT, bool RING, bool LN, bool POST>
+template <typename T, int VEC, int EPT, bool RING, bool FULL, bool LN, bool POST>
 __global__ void __maxnreg__((REGISTERS<EPT, false>)) norm_forward(const __grid_constant__ Args a) {
     extern __shared__ __align__(128) char buffers[];
     __shared__ __align__(8) unsigned long long bars[RING ? MAX_RINGS * MAX_STAGES : 1];
@@ -212,9 +227,7 @@ __global__ void __maxnreg__((REGISTERS<EPT, false>)) norm_forward(const __grid_c
     const float inv = 1.0f / (float)a.C;
     const long long rows = (long long)gridDim.x * groups;
     long long r = blockIdx.x * (long long)groups + group;
-    bool mine[NV];
-#pragma unroll
-    for (int i = 0; i < NV; i++) mine[i] = c0 + i * apart < a.C;
+    const Mine<NV, FULL> mine(c0, apart, a.C);
     int turn = 0;
     Part<T, VEC, EPT, 2, RING> next;
     next.begin(0, a.out, a.outs, r, rows, c0);
@@ -263,7 +276,7 @@ __global__ void __maxnreg__((REGISTERS<EPT, false>)) norm_forward(const __grid_c
     }
 }
 
-template <typename T, int VEC, int EPT, bool RING, bool LN, bool POST>
+template <typename T, int VEC, int EPT, bool RING, bool FULL, bool LN, bool POST>
 __global__ void __maxnreg__((REGISTERS<EPT, true>)) norm_backward(const __grid_constant__ Args a) {
     extern __shared__ __align__(128) char buffers[];
     __shared__ __align__(8) unsigned long long bars[RING ? MAX_RINGS * MAX_STAGES : 1];
@@ -273,9 +286,7 @@ __global__ void __maxnreg__((REGISTERS<EPT, true>)) norm_backward(const __grid_c
     const float inv = 1.0f / (float)a.C;
     const long long rows = (long long)gridDim.x * groups;
     long long r = blockIdx.x * (long long)groups + group;
-    bool mine[NV];
-#pragma unroll
-    for (int i = 0; i < NV; i++) mine[i] = c0 + i * apart < a.C;
+    const Mine<NV, FULL> mine(c0, apart, a.C);
     int turn = 0;
     Vec<VEC> dgamma[NV], dbeta[NV];
 #pragma unroll
@@ -402,10 +413,10 @@ long long backward_blocks(const residual_norm_s *h, long long T) {
     return need < most ? need : most;
 }
 
-template <typename T, int VEC, int EPT, bool RING, bool LN, bool POST>
+template <typename T, int VEC, int EPT, bool RING, bool FULL, bool LN, bool POST>
 cudaError_t launch_rows(const Args &a, bool backward, int grid, cudaStream_t s) {
     const int threads = block_threads(a.tpr), bytes = RING ? threads / a.tpr * a.stages * a.stage_bytes : 0;
-    const auto kernel = backward ? norm_backward<T, VEC, EPT, RING, LN, POST> : norm_forward<T, VEC, EPT, RING, LN, POST>;
+    const auto kernel = backward ? norm_backward<T, VEC, EPT, RING, FULL, LN, POST> : norm_forward<T, VEC, EPT, RING, FULL, LN, POST>;
     if (RING) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
@@ -417,9 +428,12 @@ cudaError_t launch_rows(const Args &a, bool backward, int grid, cudaStream_t s) 
 template <typename T, int VEC, bool LN, bool POST> cudaError_t launch(const Args &a, bool backward, int grid, cudaStream_t s) {
     const bool eight = values_per_thread(a.C, sizeof(T) == 4 ? SPECTRE_F32 : SPECTRE_BF16, backward) == 8;
     if constexpr (VEC > 1)
-        if (a.stages)
-            return eight ? launch_rows<T, VEC, 8, true, LN, POST>(a, backward, grid, s) : launch_rows<T, VEC, 16, true, LN, POST>(a, backward, grid, s);
-    return eight ? launch_rows<T, VEC, 8, false, LN, POST>(a, backward, grid, s) : launch_rows<T, VEC, 16, false, LN, POST>(a, backward, grid, s);
+        if (a.stages) {
+            if (a.C == a.tpr * (eight ? 8 : 16))
+                return eight ? launch_rows<T, VEC, 8, true, true, LN, POST>(a, backward, grid, s) : launch_rows<T, VEC, 16, true, true, LN, POST>(a, backward, grid, s);
+            return eight ? launch_rows<T, VEC, 8, true, false, LN, POST>(a, backward, grid, s) : launch_rows<T, VEC, 16, true, false, LN, POST>(a, backward, grid, s);
+        }
+    return eight ? launch_rows<T, VEC, 8, false, false, LN, POST>(a, backward, grid, s) : launch_rows<T, VEC, 16, false, false, LN, POST>(a, backward, grid, s);
 }
 
 template <typename T, int VEC> cudaError_t launch_norm(int norm, const Args &a, bool backward, int grid, cudaStream_t s) {
