@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Tuple
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libspectre_mix.so")
@@ -55,20 +56,6 @@ _ll = ctypes.c_longlong
 _sz = ctypes.c_size_t
 
 
-class GatedScanRows(ctypes.Structure):
-    """struct gated_scan_rows: data, batch stride and row stride (elements)."""
-    _fields_ = [("data", _vp), ("batch_stride", _ll), ("row_stride", _ll)]
-
-
-class GatedScanArgs(ctypes.Structure):
-    """struct gated_scan_args."""
-    _fields_ = [("B", _ll), ("L", _ll), ("cu_seqlens", _vp), ("nseq", _ll),
-                ("g", GatedScanRows), ("v", GatedScanRows), ("y", GatedScanRows),
-                ("dy", GatedScanRows), ("dg", GatedScanRows), ("dv", GatedScanRows),
-                ("h0", _vp), ("hT", _vp), ("dhT", _vp), ("dh0", _vp), ("states", _vp),
-                ("work", _vp), ("work_bytes", _sz), ("zero_outside", _i)]
-
-
 SIGNATURES = {
     "spectre_mix_create": (_i, [ctypes.POINTER(_vp), _i, _i, _i, _i, _i, _i, ctypes.c_float]),
     "spectre_mix_run": (_i, [_vp] * 10),
@@ -90,8 +77,8 @@ SIGNATURES = {
     "dct_mix_destroy": (_i, [_vp]),
     "gated_scan_create": (_i, [ctypes.POINTER(_vp)] + [_i] * 6),
     "gated_scan_workspace_bytes": (_sz, [_vp, _ll, _ll, _i]),
-    "gated_scan_run": (_i, [_vp, ctypes.POINTER(GatedScanArgs), _vp]),
-    "gated_scan_backward": (_i, [_vp, ctypes.POINTER(GatedScanArgs), _vp]),
+    "gated_scan_run": (_i, [_vp, ctypes.c_char_p, _vp]),
+    "gated_scan_backward": (_i, [_vp, ctypes.c_char_p, _vp]),
     "gated_scan_step": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _ll, _vp, _vp]),
     "gated_scan_destroy": (_i, [_vp]),
     "residual_norm_create": (_i, [ctypes.POINTER(_vp), _i, _i, _i, ctypes.c_float]),
@@ -520,8 +507,8 @@ def _torch_dtype(code: int):
 
 
 def _check_tensor(name, t, shape, dtype, device):
-    """A tensor's shape, type and device (``device`` None: any, for host tests)."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    """A tensor's shape (a tuple), type and device (``device`` None: any, for host tests)."""
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{name} must be {list(shape)} of {dtype}, not {list(t.shape)} of {t.dtype}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, the plan on {device}")
@@ -533,11 +520,29 @@ def _check_plain(name, t, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _rows_of(name, t) -> GatedScanRows:
-    """[B, L, N] as rows: any batch and row stride, the N values contiguous."""
-    if t.shape[2] > 1 and t.stride(2) != 1:
+def _rows_of(name, t) -> Tuple[int, int, int]:
+    """[B, L, N] as a gated_scan_rows: any batch and row stride, the N values contiguous."""
+    sb, sl, s1 = t.stride()
+    if s1 != 1 and t.shape[2] > 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    return GatedScanRows(t.data_ptr(), t.stride(0), t.stride(1))
+    return t.data_ptr(), sb, sl
+
+
+_NO_ROWS = (0, 0, 0)
+# struct gated_scan_args, packed in one go: a call's host time counts where its rows are few
+_SCAN_ARGS = struct.Struct("@qqPq" + "Pqq" * 6 + "PPPPPPNi4x")
+
+
+def gated_scan_args(B, L, g, v, y=_NO_ROWS, dy=_NO_ROWS, dg=_NO_ROWS, dv=_NO_ROWS, cu_seqlens=0, nseq=0,
+                    h0=0, hT=0, dhT=0, dh0=0, states=0, work=0, work_bytes=0, zero_outside=0) -> bytes:
+    """struct gated_scan_args; rows as (data, batch stride, row stride), pointers as
+    integers (0: NULL)."""
+    return _SCAN_ARGS.pack(B, L, cu_seqlens, nseq, *g, *v, *y, *dy, *dg, *dv, h0, hT, dhT, dh0, states,
+                           work, work_bytes, zero_outside)
+
+
+def _address(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _row_stride(name, t) -> int:
@@ -575,9 +580,9 @@ def _stream_for(stream, device, tensors) -> int:
     the work enqueued there is done."""
     import torch
 
-    current = torch._C._cuda_getCurrentRawStream(device.index)
     if stream is None:
-        return current
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    current = torch._C._cuda_getCurrentRawStream(device.index)
     raw = stream if isinstance(stream, int) else stream.cuda_stream
     if raw != current:
         if isinstance(stream, int):
@@ -605,12 +610,13 @@ def gated_scan_workspace_bytes(h: Optional[int], B: int, L: int, backward: bool)
     return int(_lib.gated_scan_workspace_bytes(h, B, L, int(backward)))
 
 
-def gated_scan_run(h: int, args: GatedScanArgs, stream: int) -> None:
-    _check(_lib.gated_scan_run(h, ctypes.byref(args), stream), "gated_scan_run")
+def gated_scan_run(h: int, args: bytes, stream: int) -> None:
+    """``args``: gated_scan_args(...)."""
+    _check(_lib.gated_scan_run(h, args, stream), "gated_scan_run")
 
 
-def gated_scan_backward(h: int, args: GatedScanArgs, stream: int) -> None:
-    _check(_lib.gated_scan_backward(h, ctypes.byref(args), stream), "gated_scan_backward")
+def gated_scan_backward(h: int, args: bytes, stream: int) -> None:
+    _check(_lib.gated_scan_backward(h, args, stream), "gated_scan_backward")
 
 
 def gated_scan_destroy(h: Optional[int]) -> None:
@@ -636,13 +642,15 @@ def check_scan_arguments(H, D, per, dtype_code, gate_code, g, v, device=None, **
     returns (B, L)."""
     if v.dim() != 3:
         raise ValueError(f"v must be [B, L, C = {H * D}]")
-    B, L = v.shape[0], v.shape[1]
-    for name, t in dict(g=g, v=v, **rows).items():
-        if t is None:
-            continue
-        gate = name in ("g", "dg")
-        width = H if gate and per == GATED_SCAN_PER["head"] else H * D
-        _check_tensor(name, t, (B, L, width), _torch_dtype(gate_code if gate else dtype_code), device)
+    B, L, _ = v.shape
+    of_v, of_g = (B, L, H * D), (B, L, H if per == GATED_SCAN_PER["head"] else H * D)
+    type_v, type_g = _torch_dtype(dtype_code), _torch_dtype(gate_code)
+    _check_tensor("v", v, of_v, type_v, device)
+    _check_tensor("g", g, of_g, type_g, device)
+    for name, t in rows.items():
+        if t is not None:
+            gate = name == "dg"
+            _check_tensor(name, t, of_g if gate else of_v, type_g if gate else type_v, device)
     return B, L
 
 
@@ -700,27 +708,30 @@ class GatedScan:
         import torch
 
         n = gated_scan_workspace_bytes(self.handle, B, L, backward)
-        return torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
+        return (torch.empty(n, dtype=torch.uint8, device=self.device), n) if n else (None, 0)
 
     def __call__(self, g, v, h0=None, cu_seqlens=None, y=None, hT=None, states=None, stream=None):
         import torch
 
-        B, L = check_scan_arguments(self.H, self.D, self.per, self.dtype_code, self.gate_code, g, v,
-                                    self.device, y=y)
-        nseq = check_scan_sequences(B, L, cu_seqlens, self.device)
+        device = self.device
+        B, L = check_scan_arguments(self.H, self.D, self.per, self.dtype_code, self.gate_code, g, v, device)
+        nseq = B if cu_seqlens is None else check_scan_sequences(B, L, cu_seqlens, device)
+        if y is not None:
+            _check_tensor("y", y, (B, L, self.C), v.dtype, device)
+        if h0 is not None or hT is not None or states is not None:
+            self._check_states(B, L, nseq, states, h0=h0, hT=hT)
+        if y is not None or hT is not None or states is not None:
+            _check_outputs([("y", y), ("hT", hT), ("states", states)], [("g", g), ("v", v), ("h0", h0)])
         made = y is None
         if made:
-            y = torch.empty((B, L, self.C), dtype=v.dtype, device=self.device)
+            y = torch.empty((B, L, self.C), dtype=v.dtype, device=device)
         if hT is None:
-            hT = torch.empty((nseq, self.C), dtype=torch.float32, device=self.device)
-        self._check_states(B, L, nseq, states, h0=h0, hT=hT)
-        _check_outputs([("y", y), ("hT", hT), ("states", states)], [("g", g), ("v", v), ("h0", h0)])
-        work = self._work(B, L, False)
-        a = GatedScanArgs(B=B, L=L, cu_seqlens=_ptr(cu_seqlens), nseq=nseq, g=_rows_of("g", g),
-                          v=_rows_of("v", v), y=_rows_of("y", y), h0=_ptr(h0), hT=_ptr(hT),
-                          states=_ptr(states), work=_ptr(work),
-                          work_bytes=0 if work is None else work.numel(), zero_outside=int(made))
-        gated_scan_run(self.handle, a, _stream_for(stream, self.device,
+            hT = torch.empty((nseq, self.C), dtype=torch.float32, device=device)
+        work, n = self._work(B, L, False)
+        a = gated_scan_args(B, L, _rows_of("g", g), _rows_of("v", v), _rows_of("y", y),
+                            cu_seqlens=_address(cu_seqlens), nseq=nseq, h0=_address(h0), hT=hT.data_ptr(),
+                            states=_address(states), work=_address(work), work_bytes=n, zero_outside=made)
+        gated_scan_run(self.handle, a, _stream_for(stream, device,
                                                    (g, v, h0, cu_seqlens, y, hT, states, work)))
         return y, hT
 
@@ -731,31 +742,32 @@ class GatedScan:
         same g, v, h0 and cu_seqlens filled."""
         import torch
 
+        device = self.device
         B, L = check_scan_arguments(self.H, self.D, self.per, self.dtype_code, self.gate_code, g, v,
-                                    self.device, dy=dy, dg=dg, dv=dv)
-        nseq = check_scan_sequences(B, L, cu_seqlens, self.device)
+                                    device, dy=dy, dg=dg, dv=dv)
+        nseq = B if cu_seqlens is None else check_scan_sequences(B, L, cu_seqlens, device)
         if states is None:
             raise ValueError("backward needs the states that the forward call filled")
         if (dg is None) != (dv is None):
             raise ValueError("dg and dv are given together or not at all")
-        made = dg is None
-        if made:
-            dg = torch.empty(g.shape, dtype=g.dtype, device=self.device)
-            dv = torch.empty((B, L, self.C), dtype=v.dtype, device=self.device)
-        if dh0 is None and h0 is not None:
-            dh0 = torch.empty((nseq, self.C), dtype=torch.float32, device=self.device)
         self._check_states(B, L, nseq, states, h0=h0, dhT=dhT, dh0=dh0)
-        _check_outputs([("dg", dg), ("dv", dv), ("dh0", dh0)],
-                       [("g", g), ("v", v), ("dy", dy), ("h0", h0), ("dhT", dhT), ("states", states)])
-        work = self._work(B, L, True)
-        a = GatedScanArgs(B=B, L=L, cu_seqlens=_ptr(cu_seqlens), nseq=nseq, g=_rows_of("g", g),
-                          v=_rows_of("v", v), dy=_rows_of("dy", dy), dg=_rows_of("dg", dg),
-                          dv=_rows_of("dv", dv), h0=_ptr(h0), dhT=_ptr(dhT), dh0=_ptr(dh0),
-                          states=_ptr(states), work=_ptr(work),
-                          work_bytes=0 if work is None else work.numel(), zero_outside=int(made))
+        made = dg is None
+        if not made or dh0 is not None:
+            _check_outputs([("dg", dg), ("dv", dv), ("dh0", dh0)],
+                           [("g", g), ("v", v), ("dy", dy), ("h0", h0), ("dhT", dhT), ("states", states)])
+        if made:
+            dg = torch.empty(g.shape, dtype=g.dtype, device=device)
+            dv = torch.empty((B, L, self.C), dtype=v.dtype, device=device)
+        if dh0 is None and h0 is not None:
+            dh0 = torch.empty((nseq, self.C), dtype=torch.float32, device=device)
+        work, n = self._work(B, L, True)
+        a = gated_scan_args(B, L, _rows_of("g", g), _rows_of("v", v), dy=_rows_of("dy", dy),
+                            dg=_rows_of("dg", dg), dv=_rows_of("dv", dv), cu_seqlens=_address(cu_seqlens),
+                            nseq=nseq, h0=_address(h0), dhT=_address(dhT), dh0=_address(dh0),
+                            states=states.data_ptr(), work=_address(work), work_bytes=n, zero_outside=made)
         gated_scan_backward(self.handle, a,
-                            _stream_for(stream, self.device, (dy, g, v, states, h0, dhT, cu_seqlens,
-                                                              dg, dv, dh0, work)))
+                            _stream_for(stream, device, (dy, g, v, states, h0, dhT, cu_seqlens,
+                                                         dg, dv, dh0, work)))
         return dg, dv, dh0
 
     def step(self, g, v, state, slots=None, y=None, new_state=None, stream=None):
@@ -766,29 +778,31 @@ class GatedScan:
         outside the pool is skipped: its y is left as it is, or zero where y is made here."""
         import torch
 
-        B = v.shape[0]
-        width = self.H if self.per == GATED_SCAN_PER["head"] else self.C
-        _check_tensor("g", g, (B, width), _torch_dtype(self.gate_code), self.device)
-        _check_tensor("v", v, (B, self.C), _torch_dtype(self.dtype_code), self.device)
-        if y is None:
-            y = (torch.empty if slots is None else torch.zeros)((B, self.C), dtype=v.dtype, device=self.device)
-        _check_tensor("y", y, (B, self.C), v.dtype, self.device)
+        device, B, C = self.device, v.shape[0], self.C
+        _check_tensor("g", g, (B, self.H if self.per == GATED_SCAN_PER["head"] else C),
+                      _torch_dtype(self.gate_code), device)
+        _check_tensor("v", v, (B, C), _torch_dtype(self.dtype_code), device)
         S = state.shape[0]
-        _check_plain("state", state, (S, self.C), torch.float32, self.device)
+        _check_plain("state", state, (S, C), torch.float32, device)
         if new_state is None:
             new_state = state
-        _check_plain("new_state", new_state, (S, self.C), torch.float32, self.device)
+        else:
+            _check_plain("new_state", new_state, (S, C), torch.float32, device)
         if slots is not None:
-            _check_plain("slots", slots, (B,), torch.int32, self.device)
+            _check_plain("slots", slots, (B,), torch.int32, device)
         elif S < B:
             raise ValueError(f"state holds {S} rows, the step has {B}")
-        for name, t in (("g", g), ("v", v), ("y", y)):
-            if t.shape[1] > 1 and t.stride(1) != 1:
-                raise ValueError(f"the last dimension of {name} must be contiguous")
-        _check_outputs([("y", y)], [("g", g), ("v", v), ("state", state), ("new_state", new_state)])
-        raw = _stream_for(stream, self.device, (g, v, state, slots, y, new_state))
-        _check(_lib.gated_scan_step(self.handle, B, g.data_ptr(), g.stride(0), v.data_ptr(), v.stride(0),
-                                    state.data_ptr(), S, _ptr(slots), y.data_ptr(), y.stride(0),
+        if y is None:
+            y = (torch.empty if slots is None else torch.zeros)((B, C), dtype=v.dtype, device=device)
+        else:
+            _check_tensor("y", y, (B, C), v.dtype, device)
+            _check_outputs([("y", y)], [("g", g), ("v", v), ("state", state), ("new_state", new_state)])
+        (gs, g1), (vs, v1), (ys, y1) = g.stride(), v.stride(), y.stride()
+        if (g1 != 1 and g.shape[1] > 1) or (C > 1 and not v1 == y1 == 1):
+            raise ValueError("the last dimension of g, v and y must be contiguous")
+        raw = _stream_for(stream, device, (g, v, state, slots, y, new_state))
+        _check(_lib.gated_scan_step(self.handle, B, g.data_ptr(), gs, v.data_ptr(), vs, state.data_ptr(), S,
+                                    None if slots is None else slots.data_ptr(), y.data_ptr(), ys,
                                     new_state.data_ptr(), raw), "gated_scan_step")
         return y, new_state
 
@@ -843,7 +857,7 @@ def check_norm_arguments(C, dtype_code, device=None, vectors=(), **rows) -> Tupl
         if shape is None:
             if t.dim() < 1 or t.shape[-1] != C:
                 raise ValueError(f"{name} must be [..., C = {C}]")
-            shape = tuple(t.shape)
+            shape = t.shape
         _check_tensor(name, t, shape, _torch_dtype(dtype_code), device)
     for name, t in vectors:
         if t is not None:
@@ -877,11 +891,12 @@ class ResidualNorm:
     def __call__(self, out, x, gamma, beta, y=None, stream=None):
         import torch
 
-        if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         check_norm_arguments(self.C, self.dtype_code, self.device, (("gamma", gamma), ("beta", beta)),
                              out=out, x=x, y=y)
-        _check_outputs([("y", y)], [("out", out), ("x", x)])
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=self.device)
+        else:
+            _check_outputs([("y", y)], [("out", out), ("x", x)])
         raw = _stream_for(stream, self.device, (out, x, gamma, beta, y))
         _check(_lib.residual_norm_run(self.handle, x.numel() // self.C, out.data_ptr(), _row_stride("out", out),
                                       x.data_ptr(), _row_stride("x", x), gamma.data_ptr(), beta.data_ptr(),
@@ -893,17 +908,18 @@ class ResidualNorm:
 
         if self.post and x is None:
             raise ValueError("the post forms' gradient needs x")
-        if dout is None:
-            dout = torch.empty(out.shape, dtype=out.dtype, device=out.device)
-        if dgamma is None:
-            dgamma = torch.empty(self.C, dtype=torch.float32, device=out.device)
-        if dbeta is None:
-            dbeta = torch.empty(self.C, dtype=torch.float32, device=out.device)
         check_norm_arguments(self.C, self.dtype_code, self.device,
                              (("gamma", gamma), ("dgamma", dgamma), ("dbeta", dbeta)),
                              dy=dy, out=out, x=x, dout=dout)
-        _check_outputs([("dout", dout), ("dgamma", dgamma), ("dbeta", dbeta)],
-                       [("dy", dy), ("out", out), ("x", x), ("gamma", gamma)])
+        if dout is not None or dgamma is not None or dbeta is not None:
+            _check_outputs([("dout", dout), ("dgamma", dgamma), ("dbeta", dbeta)],
+                           [("dy", dy), ("out", out), ("x", x), ("gamma", gamma)])
+        if dout is None:
+            dout = torch.empty(out.shape, dtype=out.dtype, device=self.device)
+        if dgamma is None:
+            dgamma = torch.empty(self.C, dtype=torch.float32, device=self.device)
+        if dbeta is None:
+            dbeta = torch.empty(self.C, dtype=torch.float32, device=self.device)
         T = out.numel() // self.C
         n = residual_norm_workspace_bytes(self.handle, T)
         work = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None

@@ -231,15 +231,6 @@ __device__ __forceinline__ float mul0(float a, float h) { return a == 0.0f ? 0.0
 __device__ __forceinline__ float fma0(float a, float h, float b) { return a == 0.0f ? b : fmaf(a, h, b); }
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __int_as_float(0x7f800000); }
 
-template <int FORM> __device__ __forceinline__ float input_of(Gate k, float v) {
-    return FORM == GATED_SCAN_EXP ? v : mul0(k.c, v);
-}
-// d(h_t) / d(g_t) from the state before the row
-template <int FORM> __device__ __forceinline__ float slope_of(Gate k, float before, float v) {
-    return FORM == GATED_SCAN_EXP ? mul0(k.a, before) : mul0(k.a * k.c, before - v);
-}
-
-
 // A tile: CHUNK rows of WIDTH channels, 128 bytes of a row.  V channels a thread: 4 where rows and
 // heads allow it, else 1 (then a row's part is 32 channels and a thread has 16 rows).
 template <typename TV, int V> struct Tile {
@@ -261,9 +252,10 @@ struct Args {
     unsigned long long head_of;   // ceil(2^40 / D): c * head_of >> 40 = c / D for c <= 2^20
     int strips;               // tiles beside one another: ceil(C / WIDTH)
     int nchunk;
+    int serial;               // a block takes whole strips
     int nsm;
     long long nseq;           // dense: B
-    unsigned long long *words;   // null where a sequence has one chunk
+    unsigned long long *words;   // null where no tile waits for another
     float *parts;             // per-head gradients of heads that span strips: [pieces][B L][H]
 };
 
@@ -374,7 +366,9 @@ __device__ __forceinline__ void look_back(LookBack<WIDTH, QS> &m, const unsigned
 
 // Where the block's tile lies.  Tiles are numbered chunk by chunk over all batch entries and
 // strips, in the direction of the walk, so that every strip advances at the same time; a block
-// takes every gridDim.x-th, and goes from one to the next without a division.
+// takes every gridDim.x-th, and goes from one to the next without a division.  Where there are
+// strips enough, or few chunks, a block takes a strip's chunks one after another instead and
+// carries the state itself.
 struct Place {
     int i, b, strip;   // i: the chunk in walking order
     __device__ __forceinline__ Place() {}
@@ -385,11 +379,16 @@ struct Place {
         strip = (int)(rest % strips);
     }
     __device__ __forceinline__ void advance(const Args &p, const Place &by) {
+        if (p.serial) {   // the strip's next chunk, or another strip
+            if (++i < p.nchunk) return;
+            i = by.i ? p.nchunk : 0;
+        } else {
+            i += by.i;
+        }
         strip += by.strip;
         b += by.b;
-        i += by.i;
         if (strip >= p.strips) strip -= p.strips, b++;
-        if (b >= (int)p.a.B) b -= (int)p.a.B, i++;
+        if (b >= (int)p.a.B) b -= (int)p.a.B, i = p.serial ? p.nchunk : i + 1;
     }
     __device__ __forceinline__ long long first_word(const Args &p) const { return ((long long)b * p.strips + strip) * p.nchunk; }
 };
@@ -511,9 +510,10 @@ template <typename TV, typename TG, bool HEAD, int V> struct Rows {
 
 // Blocks an SM.
 template <typename TV, bool HEAD> constexpr int FORWARD_BLOCKS = HEAD && sizeof(TV) == 4 ? 5 : 3;
+constexpr int SINGLE_BLOCKS = 2;   // channels one by one
 
 template <typename TV, typename TG, int FORM, bool HEAD, int V>
-__global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? 2 : FORWARD_BLOCKS<TV, HEAD>)
+__global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS : FORWARD_BLOCKS<TV, HEAD>)
     scan_forward(const __grid_constant__ Args p, const __grid_constant__ Maps maps) {
     using S = Tile<TV, V>;
     using M = Stage<TV, TG, HEAD, V>;
@@ -532,7 +532,8 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? 2 : FORWARD_BLO
     Place next(p, blockIdx.x);
     const Place by(p, gridDim.x);
     // more tiles of a strip in flight than one thread's REACH: ask far at once
-    const bool far = (unsigned)(p.a.B * p.strips) * REACH < gridDim.x;
+    const bool far = !p.serial && (unsigned)(p.a.B * p.strips) * REACH < gridDim.x;
+    float carry = 0.0f;   // serial: a channel's state (or gradient) behind the last tile
 
     const bool agent = threadIdx.x == S::THREADS - 32;   // issues all copies
     auto fetch = [&](const Place &at, int turn) {
@@ -650,9 +651,10 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? 2 : FORWARD_BLO
                     M::keep(pg, pv, r, lastP);
                 else if constexpr (M::ON)
                     head_P[r][threadIdx.x] = lastP[0];
-                else
+                else {
 #pragma unroll
                     for (int j = 0; j < GV; j++) P[r][j] = lastP[j];
+                }
 #pragma unroll
                 for (int j = 0; j < V; j++) Q[r][j] = q[j];
             }
@@ -685,7 +687,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? 2 : FORWARD_BLO
         fetch_gates(next);
         const int x = threadIdx.x, cx = c0 + threadIdx.x % S::WIDTH;
         unsigned long long *const words = p.words + at.first_word(p) * S::WIDTH;
-        const bool more = at.i + 1 < p.nchunk;
+        const bool more = !p.serial && at.i + 1 < p.nchunk;
         float allP = 1.0f, allQ = 0.0f;
         if (x < S::WIDTH) {
             // each group's pair becomes that of all groups ahead of it
@@ -702,7 +704,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? 2 : FORWARD_BLO
         if (at.i > 0 && far) {
             look_back(ahead, words, at.i, cx < p.C);
         } else if (at.i > 0) {
-            if (x < S::WIDTH) ahead.state[x] = cx < p.C ? look_near<S::WIDTH>(words + x, at.i) : 0.0f;
+            if (x < S::WIDTH) ahead.state[x] = p.serial ? carry : cx < p.C ? look_near<S::WIDTH>(words + x, at.i) : 0.0f;
             __syncthreads();
         } else {
             if (x < S::WIDTH) ahead.state[x] = !packed && p.a.h0 && cx < p.C ? p.a.h0[at.b * p.C + cx] : 0.0f;
@@ -710,7 +712,8 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? 2 : FORWARD_BLO
         }
         if (x < S::WIDTH && cx < p.C) {
             const float state = ahead.state[x];
-            if (more) publish(words + (long long)at.i * S::WIDTH + x, 0.0f, fma0(allP, state, allQ));
+            carry = fma0(allP, state, allQ);
+            if (more) publish(words + (long long)at.i * S::WIDTH + x, 0.0f, carry);
             if (p.a.states) p.a.states[(at.b * p.nchunk + at.i) * p.C + cx] = state;
         }
 
@@ -808,7 +811,8 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
     const int lane = threadIdx.x % S::LANES, group = threadIdx.x / S::LANES;
     Place next(p, blockIdx.x);
     const Place by(p, gridDim.x);
-    const bool far = (unsigned)(p.a.B * p.strips) * REACH < gridDim.x;
+    const bool far = !p.serial && (unsigned)(p.a.B * p.strips) * REACH < gridDim.x;
+    float carry = 0.0f;   // serial: a channel's state (or gradient) behind the last tile
 
     const bool agent = threadIdx.x == S::THREADS - 32;   // issues all copies
     auto fetch = [&](const Place &at, int turn) {
@@ -1007,7 +1011,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
         fetch_gates(next);
         const int x = threadIdx.x, cx = c0 + threadIdx.x % S::WIDTH;
         unsigned long long *const words = p.words + at.first_word(p) * S::WIDTH;
-        const bool more = at.i + 1 < p.nchunk;
+        const bool more = !p.serial && at.i + 1 < p.nchunk;
         float allT = 1.0f, allE = 0.0f;
         if (x < S::WIDTH) {
             // each group's pair becomes that of all groups ahead of it, going back
@@ -1040,13 +1044,16 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
         if (at.i > 0 && far) {
             look_back(ahead, words, at.i, cx < p.C);
         } else if (at.i > 0) {
-            if (x < S::WIDTH) ahead.state[x] = cx < p.C ? look_near<S::WIDTH>(words + x, at.i) : 0.0f;
+            if (x < S::WIDTH) ahead.state[x] = p.serial ? carry : cx < p.C ? look_near<S::WIDTH>(words + x, at.i) : 0.0f;
             __syncthreads();
         } else {
             if (x < S::WIDTH) ahead.state[x] = 0.0f;
             __syncthreads();
         }
-        if (x < S::WIDTH && cx < p.C && more) publish(words + (long long)at.i * S::WIDTH + x, 0.0f, fma0(allT, ahead.state[x], allE));
+        if (x < S::WIDTH && cx < p.C) {
+            carry = fma0(allT, ahead.state[x], allE);
+            if (more) publish(words + (long long)at.i * S::WIDTH + x, 0.0f, carry);
+        }
 
         float h[V], e[V];
         {
@@ -1242,28 +1249,51 @@ template <typename TG> __global__ void join_parts(Args p, int width) {
     row<TG>(p.a.dg, b, t)[h] = from_f<TG>(s);
 }
 
-// One token: thread (i, c); a slot named by an earlier row is that row's to finish.
-template <typename TV, typename TG, int FORM>
-__global__ void scan_step(long long B, int C, int D, int per, const TG *g, long long gs, const TV *v,
-                          long long vs, const float *state, long long S, const int *slots, TV *y,
-                          long long ys, float *next) {
-    const int c = blockIdx.y * blockDim.x + threadIdx.x;
-    const long long i0 = blockIdx.x;
+// One token.  A block has a row and STEP_THREADS * V channels of it; the loads that decide nothing
+// come first.  Rows of one slot belong to the first of them, which takes the others in order: every
+// block looks through the slots for rows ahead of its own and behind it (B words from the caches).
+constexpr int STEP_THREADS = 128;
+template <typename TV, typename TG, int FORM, bool HEAD, int V>
+__global__ void __launch_bounds__(STEP_THREADS) scan_step(int B, int C, int D, const TG *g, long long gs, const TV *v, long long vs,
+                                                          const float *state, long long S, const int *slots, TV *y, long long ys, float *next) {
+    constexpr int GV = HEAD ? 1 : V;
+    const int c = (blockIdx.y * STEP_THREADS + threadIdx.x) * V, i0 = blockIdx.x;
+    const int gc = HEAD ? c / D : c;
     const long long slot = slots ? slots[i0] : i0;
-    if (slot < 0 || slot >= S) return;
-    bool first = true;
-    if (slots)
-        for (long long j = 0; j < i0; j++) first &= slots[j] != slot;
-    if (!first || c >= C) return;
-    const int gc = per == GATED_SCAN_PER_HEAD ? c / D : c;
-    float h = state[slot * C + c];
-    for (long long i = i0; i < B; i++) {
-        if (i != i0 && (!slots || slots[i] != slot)) continue;
-        const Gate k = gate_of<FORM, false>(to_f(g[i * gs + gc]));
-        h = fma0(k.a, h, input_of<FORM>(k, to_f(v[i * vs + c])));
-        y[i * ys + c] = from_f<TV>(h);
+    const bool there = slot >= 0 && slot < S;
+    Pack<float, V> h;
+    Pack<TG, GV> gi;
+    Pack<TV, V> vi;
+    if (there && c < C) {
+        h = load<float, V>(state + slot * C + c);
+        gi = load<TG, GV>(g + i0 * gs + gc);
+        vi = load<TV, V>(v + i0 * vs + c);
     }
-    next[slot * C + c] = h;
+    bool behind = false;
+    if (slots) {
+        bool before = false;
+        for (int j = threadIdx.x; j < B; j += STEP_THREADS)
+            if (j != i0 && slots[j] == slot) (j < i0 ? before : behind) = true;
+        if (__syncthreads_or(before)) return;
+        behind = __syncthreads_or(behind);
+    }
+    if (!there || c >= C) return;
+    for (int i = i0;;) {
+        float f[V];
+#pragma unroll
+        for (int j = 0; j < V; j++) {
+            const Gate k = gate_of<FORM, false>(to_f(gi.v[HEAD ? 0 : j]));
+            h.v[j] = f[j] = fma0(k.a, h.v[j], FORM == GATED_SCAN_EXP ? to_f(vi.v[j]) : mul0(k.c, to_f(vi.v[j])));
+        }
+        store<TV, V>(y + i * ys + c, f);
+        if (!behind) break;
+        do i++;
+        while (i < B && slots[i] != slot);
+        if (i >= B) break;
+        gi = load<TG, GV>(g + i * gs + gc);
+        vi = load<TV, V>(v + i * vs + c);
+    }
+    *reinterpret_cast<Pack<float, V> *>(next + slot * C + c) = h;
 }
 
 // what one output of `width` values a row needs for its rows to lie apart
@@ -1298,13 +1328,29 @@ int pieces_of(const gated_scan_s *h, int V) {
     return most;
 }
 
+// Blocks an SM that the kernels are built for.
+int blocks_per_sm(const gated_scan_s *h, bool backward, int V) {
+    if (backward) return BACKWARD_BLOCKS;
+    if (V == 1) return SINGLE_BLOCKS;
+    const bool head = h->per == GATED_SCAN_PER_HEAD;
+    return h->dtype == SPECTRE_F32 ? (head ? FORWARD_BLOCKS<float, true> : FORWARD_BLOCKS<float, false>)
+                                   : (head ? FORWARD_BLOCKS<__nv_bfloat16, true> : FORWARD_BLOCKS<__nv_bfloat16, false>);
+}
+
 struct Work {
+    bool serial;                  // a block takes whole strips: no words, and an ordinary launch
     size_t words, parts, bytes;   // offset of the parts, the whole
 };
 Work work_of(const gated_scan_s *h, long long B, long long L, bool backward, int V) {
-    const size_t nchunk = (L + CHUNK - 1) / CHUNK;
+    const long long nchunk = (L + CHUNK - 1) / CHUNK, strips = B * strips_of(h, V);
+    const long long most = (long long)h->nsm * blocks_per_sm(h, backward, V);
+    // In tiles that the busiest block takes.  Looking back costs each tile about a sixth more and
+    // the launch about two tiles (the words to clear, the blocks to start together): 256 rows of 16
+    // channels take 9.9 us by look back and 8.0 us in one strip's order, 1,024 rows 13.9 and 18.9.
+    const long long one = (strips + most - 1) / most * nchunk, all = (strips * nchunk + most - 1) / most;
     Work w{};
-    if (nchunk > 1) w.words = ((size_t)B * strips_of(h, V) * nchunk + AHEAD) * width_of(h, V) * 8;
+    w.serial = one * 6 <= all * 7 + 12;
+    if (!w.serial) w.words = ((size_t)strips * nchunk + AHEAD) * width_of(h, V) * 8;
     w.words = (w.words + 255) / 256 * 256;
     const int pieces = backward ? pieces_of(h, V) : 1;
     if (pieces > 1) w.parts = (size_t)pieces * B * L * h->H * sizeof(float);
@@ -1398,10 +1444,11 @@ cudaError_t launch_tiles(Args &p, bool backward, const Work &w, cudaStream_t s) 
                                   resident(scan_backward<TV, TG, FORM, HEAD, V>, S::THREADS, M::ON ? 2 * (M::INPUT_BYTES + M::V_BYTES) : 0)};
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    const long long most = (long long)p.nsm * per_sm[backward];
+    const long long most = (long long)p.nsm * per_sm[backward], blocks = w.serial ? p.a.B * p.strips : tiles;
+    p.serial = w.serial;
     if (!most) return cudaErrorUnknown;
     cudaLaunchConfig_t config{};
-    config.gridDim = dim3((unsigned)(tiles < most ? tiles : most));
+    config.gridDim = dim3((unsigned)(blocks < most ? blocks : most));
     config.blockDim = dim3(S::THREADS);
     config.dynamicSmemBytes = bytes;
     config.stream = s;
@@ -1493,14 +1540,12 @@ int run(gated_scan_s *h, const gated_scan_args *a, bool backward, void *stream) 
                                                : launch_types<GATED_SCAN_SIGMOID>(h, p, V, backward, work, s));
 }
 
-template <typename TV, typename TG, int FORM>
-cudaError_t launch_step(const gated_scan_s *h, long long B, const void *g, long long gs, const void *v,
-                        long long vs, const float *state, long long S, const int *slots, void *y,
-                        long long ys, float *next, cudaStream_t s) {
-    const dim3 grid((unsigned)B, (h->C + 127) / 128);
-    scan_step<TV, TG, FORM><<<grid, 128, 0, s>>>(B, h->C, h->D, h->per, static_cast<const TG *>(g), gs,
-                                                 static_cast<const TV *>(v), vs, state, S, slots,
-                                                 static_cast<TV *>(y), ys, next);
+template <typename TV, typename TG, int FORM, bool HEAD, int V>
+cudaError_t launch_step(const gated_scan_s *h, long long B, const void *g, long long gs, const void *v, long long vs,
+                        const float *state, long long S, const int *slots, void *y, long long ys, float *next, cudaStream_t s) {
+    const dim3 grid((unsigned)B, (h->C + STEP_THREADS * V - 1) / (STEP_THREADS * V));
+    scan_step<TV, TG, FORM, HEAD, V><<<grid, STEP_THREADS, 0, s>>>((int)B, h->C, h->D, static_cast<const TG *>(g), gs, static_cast<const TV *>(v), vs,
+                                                                   state, S, slots, static_cast<TV *>(y), ys, next);
     return cudaGetLastError();
 }
 
@@ -1553,13 +1598,26 @@ int gated_scan_step(gated_scan_t h, long long B, const void *g, long long g_stri
     if (!current_device_is(h->device)) return SPECTRE_ERR_DEVICE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     using bf = __nv_bfloat16;
-    auto go = [&](auto fn) { return status_of(fn(h, B, g, g_stride, v, v_stride, state, S, slots, y, y_stride, new_state, s)); };
-    const bool e = h->gate == GATED_SCAN_EXP;
-    if (h->dtype == SPECTRE_F32)
-        return e ? go(launch_step<float, float, GATED_SCAN_EXP>) : go(launch_step<float, float, GATED_SCAN_SIGMOID>);
-    if (h->gate_dtype == SPECTRE_F32)
-        return e ? go(launch_step<bf, float, GATED_SCAN_EXP>) : go(launch_step<bf, float, GATED_SCAN_SIGMOID>);
-    return e ? go(launch_step<bf, bf, GATED_SCAN_EXP>) : go(launch_step<bf, bf, GATED_SCAN_SIGMOID>);
+    const bool head = h->per == GATED_SCAN_PER_HEAD;
+    const auto four = [](const void *p, long long stride, size_t es) { return aligned(p, 4 * es) && stride % 4 == 0; };
+    const bool vec = (head ? h->D : h->C) % 4 == 0 && four(v, v_stride, ev) && four(y, y_stride, ev) && (head || four(g, g_stride, eg)) &&
+                     aligned(state, 16) && aligned(new_state, 16);
+    auto go = [&](auto tv, auto tg, auto form, auto hd, auto four) {
+        return status_of(launch_step<decltype(tv), decltype(tg), decltype(form)::value, decltype(hd)::value, decltype(four)::value>(
+            h, B, g, g_stride, v, v_stride, state, S, slots, y, y_stride, new_state, s));
+    };
+    auto go_shape = [&](auto tv, auto tg, auto form) {
+        using one = std::integral_constant<int, 1>;
+        using many = std::integral_constant<int, 4>;
+        if (head) return vec ? go(tv, tg, form, std::true_type{}, many{}) : go(tv, tg, form, std::true_type{}, one{});
+        return vec ? go(tv, tg, form, std::false_type{}, many{}) : go(tv, tg, form, std::false_type{}, one{});
+    };
+    auto go_types = [&](auto form) {
+        if (h->dtype == SPECTRE_F32) return go_shape(0.0f, 0.0f, form);
+        if (h->gate_dtype == SPECTRE_F32) return go_shape(bf(), 0.0f, form);
+        return go_shape(bf(), bf(), form);
+    };
+    return h->gate == GATED_SCAN_EXP ? go_types(std::integral_constant<int, GATED_SCAN_EXP>{}) : go_types(std::integral_constant<int, GATED_SCAN_SIGMOID>{});
 }
 
 int gated_scan_destroy(gated_scan_t h) {

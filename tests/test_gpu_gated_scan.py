@@ -498,22 +498,20 @@ def test_refusals():
         with pytest.raises(ValueError):
             s.step(gd[:, 0], vd[:, 0], torch.zeros(2, 16, device="cuda"), y=vd[:, 0])
         # the C entry points: short or misaligned workspaces, misaligned rows
-        a = b.GatedScanArgs(B=2, L=20, g=b.GatedScanRows(gd.data_ptr() + 1, 320, 16), v=b._rows_of("v", vd),
-                            y=b._rows_of("y", torch.empty_like(vd)))
-        assert b._lib.gated_scan_run(s.handle, a, None) == b.SPECTRE_ERR_ALIGN
-        a.g.data = gd.data_ptr()
-        a.B = -1
-        assert b._lib.gated_scan_run(s.handle, a, None) == b.SPECTRE_ERR_ARG
-        a.B, a.L = 1 << 40, 1 << 40
-        assert b._lib.gated_scan_run(s.handle, a, None) == b.SPECTRE_ERR_ARG
+        def run(B=2, L=20, g=(gd.data_ptr(), 320, 16)):
+            a = b.gated_scan_args(B, L, g, b._rows_of("v", vd), b._rows_of("y", torch.empty_like(vd)))
+            return b._lib.gated_scan_run(s.handle, a, None)
+        assert run(g=(gd.data_ptr() + 1, 320, 16)) == b.SPECTRE_ERR_ALIGN
+        assert run(g=(gd.data_ptr(), 320, -16)) == b.SPECTRE_ERR_ARG and run(g=(0, 320, 16)) == b.SPECTRE_ERR_ARG
+        assert run(B=-1) == b.SPECTRE_ERR_ARG and run(B=1 << 40, L=1 << 40) == b.SPECTRE_ERR_ARG
     with b.GatedScan(2, 160, "f32", "exp", "head") as s:
         need = b.gated_scan_workspace_bytes(s.handle, 1, 4, True)
         t = [torch.zeros(1, 4, n, device="cuda") for n in (2, 320, 320, 2, 320)]
         st = s.new_states(1, 4)
         work = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
         r = [b._rows_of("t", x) for x in t]
-        a = b.GatedScanArgs(B=1, L=4, g=r[0], v=r[1], dy=r[2], dg=r[3], dv=r[4], states=st.data_ptr(),
-                            work=work.data_ptr(), work_bytes=need - 1)
-        assert b._lib.gated_scan_backward(s.handle, a, None) == b.SPECTRE_ERR_ARG
-        a.work, a.work_bytes = work.data_ptr() + 4, need
-        assert b._lib.gated_scan_backward(s.handle, a, None) == b.SPECTRE_ERR_ALIGN
+        def back(w, n):
+            a = b.gated_scan_args(1, 4, r[0], r[1], dy=r[2], dg=r[3], dv=r[4], states=st.data_ptr(), work=w, work_bytes=n)
+            return b._lib.gated_scan_backward(s.handle, a, None)
+        assert back(work.data_ptr(), need - 1) == b.SPECTRE_ERR_ARG
+        assert back(work.data_ptr() + 4, need) == b.SPECTRE_ERR_ALIGN

@@ -23,10 +23,32 @@ def test_every_declared_function_is_exported_and_bound(header, prefix):
         assert hasattr(lib, n) and n in b.SIGNATURES, n
 
 
-def test_structures_have_the_header_sizes():
-    # three 8-byte members, and the args' 4 scalars, 6 rows, 5 pointers, workspace and flag
-    assert ctypes.sizeof(b.GatedScanRows) == 24
-    assert ctypes.sizeof(b.GatedScanArgs) == 4 * 8 + 6 * 24 + 5 * 8 + 8 + 8 + 8
+def test_packed_arguments_have_the_header_layout():
+    """The bytes that the binding packs, against the structure as a C compiler lays it out."""
+    class Rows(ctypes.Structure):
+        _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_longlong), ("row_stride", ctypes.c_longlong)]
+
+    class Args(ctypes.Structure):
+        _fields_ = ([("B", ctypes.c_longlong), ("L", ctypes.c_longlong), ("cu_seqlens", ctypes.c_void_p), ("nseq", ctypes.c_longlong)] +
+                    [(n, Rows) for n in ("g", "v", "y", "dy", "dg", "dv")] +
+                    [(n, ctypes.c_void_p) for n in ("h0", "hT", "dhT", "dh0", "states", "work")] +
+                    [("work_bytes", ctypes.c_size_t), ("zero_outside", ctypes.c_int)])
+
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "gated_scan.h")).read(), flags=re.S)
+    body = re.search(r"typedef struct gated_scan_args \{(.*?)\}", text, re.S).group(1)
+    names = [n for line in body.split(";") for n in re.findall(r"\b(\w+)\s*(?=,|$)", line.strip())]
+    assert names == [n for n, _ in Args._fields_]
+    rows = {n: (100 * i + 1, 100 * i + 2, 100 * i + 3) for i, n in enumerate(("g", "v", "y", "dy", "dg", "dv"))}
+    rest = {n: 1000 + i for i, n in enumerate(("cu_seqlens", "nseq", "h0", "hT", "dhT", "dh0", "states", "work", "work_bytes"))}
+    packed = b.gated_scan_args(7, 8, **rows, **rest, zero_outside=True)
+    assert len(packed) == ctypes.sizeof(Args)
+    a = Args.from_buffer_copy(packed)
+    assert (a.B, a.L, a.zero_outside) == (7, 8, 1)
+    for n, want in rest.items():
+        assert getattr(a, n) == want, n
+    for n, want in rows.items():
+        r = getattr(a, n)
+        assert (r.data, r.batch_stride, r.row_stride) == want, n
 
 
 @pytest.mark.parametrize("args", [(0, 4, 0, 0, 0, 0), (4, 0, 0, 0, 0, 0), (2048, 1024, 0, 0, 0, 0),
@@ -45,9 +67,9 @@ def test_norm_create_refuses(args):
 
 
 def test_null_handles():
-    a = b.GatedScanArgs()
-    assert b._lib.gated_scan_run(None, ctypes.byref(a), None) == b.SPECTRE_ERR_ARG
-    assert b._lib.gated_scan_backward(None, ctypes.byref(a), None) == b.SPECTRE_ERR_ARG
+    a = b.gated_scan_args(1, 1, (0, 0, 0), (0, 0, 0))
+    assert b._lib.gated_scan_run(None, a, None) == b.SPECTRE_ERR_ARG
+    assert b._lib.gated_scan_backward(None, a, None) == b.SPECTRE_ERR_ARG
     assert b._lib.gated_scan_step(None, 1, None, 0, None, 0, None, 0, None, None, 0, None, None) == b.SPECTRE_ERR_ARG
     assert b.gated_scan_workspace_bytes(None, 1, 1, True) == 0
     assert b._lib.residual_norm_run(None, 1, None, 0, None, 0, None, None, None, 0, None) == b.SPECTRE_ERR_ARG
@@ -94,8 +116,7 @@ def test_sequences():
 
 def test_rows_and_strides():
     t = torch.zeros(3, 5, 16)
-    r = b._rows_of("t", t[:, :, 8:])
-    assert (r.batch_stride, r.row_stride) == (80, 16) and r.data == t.data_ptr() + 32
+    assert b._rows_of("t", t[:, :, 8:]) == (t.data_ptr() + 32, 80, 16)
     with pytest.raises(ValueError):
         b._rows_of("t", t.transpose(1, 2))
     assert b._row_stride("t", t) == 16 and b._row_stride("t", t[..., :7]) == 16
