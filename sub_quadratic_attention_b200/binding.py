@@ -547,10 +547,10 @@ def _address(t) -> int:
 
 def _row_stride(name, t) -> int:
     """[..., N] as rows with one stride between them; raises where they have none."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
     if t.is_contiguous():
         return t.shape[-1]
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
     stride, extent = None, 1
     for size, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
         if size == 1:
@@ -850,15 +850,15 @@ def check_norm_arguments(C, dtype_code, device=None, vectors=(), **rows) -> Tupl
     that shape."""
     import torch
 
-    shape = None
+    shape, dtype = None, _torch_dtype(dtype_code)
     for name, t in rows.items():
         if t is None:
             continue
         if shape is None:
-            if t.dim() < 1 or t.shape[-1] != C:
-                raise ValueError(f"{name} must be [..., C = {C}]")
             shape = t.shape
-        _check_tensor(name, t, shape, _torch_dtype(dtype_code), device)
+            if not shape or shape[-1] != C:
+                raise ValueError(f"{name} must be [..., C = {C}]")
+        _check_tensor(name, t, shape, dtype, device)
     for name, t in vectors:
         if t is not None:
             _check_plain(name, t, (C,), torch.float32, device)

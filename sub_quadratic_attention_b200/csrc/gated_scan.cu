@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
         // row r's state is P[r] h + Q[r], h the state ahead of the thread's rows
         [[maybe_unused]] float P[M::ON ? 1 : S::ROWS][GV];
         float Q[S::ROWS][V], lastP[GV];
-        auto walk = [&](auto careful) {
+        auto walk = [&](auto careful, bool again) {
             constexpr bool CARE = decltype(careful)::value;   // rows that are missing, starts, factors of zero
             float q[V];
 #pragma unroll
@@ -598,8 +598,8 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
             for (int j = 0; j < V; j++) q[j] = 0.0f;
             const TG *gp = rows.template first<TG>(p.a.g, rows.gc);
             const TV *vp = rows.template first<TV>(p.a.v, c);
-            // all rows first: what is kept goes where they stand.  A careful walk may be a second
-            // one and reads them from memory again, row by row.
+            // all rows first: what is kept goes where they stand.  A careful walk that is a second
+            // one reads them from memory again.
             Pack<TG, GV> gs[S::ROWS];
             Pack<TV, V> vs[S::ROWS];
             if constexpr (!CARE) {
@@ -626,8 +626,11 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
                 }
                 if (!CARE || (r < rows.count && rows.t0 + r >= lo && rows.t0 + r < hi)) {
                     if constexpr (CARE) {
-                        gs[r] = load<TG, GV>(gp + r * p.a.g.row_stride);
-                        vs[r] = load<TV, V>(vp + r * p.a.v.row_stride);
+                        const bool memory = again || !M::ON;
+                        if constexpr (HEAD && M::ON) gs[r].v[0] = g_now[r];
+                        else gs[r] = load<TG, GV>(memory ? gp + r * p.a.g.row_stride : reinterpret_cast<const TG *>(pg + M::at_g(r)));
+                        vs[r] = load<TV, V>(memory ? vp + r * p.a.v.row_stride : reinterpret_cast<const TV *>(pv + M::at_v(r)));
+                        asm volatile("" ::: "memory");
                     }
                     const Pack<TG, GV> &g = gs[r];
                     const Pack<TV, V> &v = vs[r];
@@ -665,11 +668,11 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
         // the rows are walked again.
         bool fine = plain && arrived;
         if (fine) {
-            walk(std::false_type{});
+            walk(std::false_type{}, false);
 #pragma unroll
             for (int j = 0; j < V; j++) fine &= finite(Q[S::ROWS - 1][j]);
         }
-        if (!fine) walk(std::true_type{});
+        if (!fine) walk(std::true_type{}, plain || !arrived);
         {
             float lp[V], lq[V];
 #pragma unroll
@@ -853,7 +856,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
         const int c0 = rows.c0, c = rows.c;
         const long long tile0 = (long long)rows.chunk * CHUNK;
         long long lo = 0, hi = p.a.L;
-        bool edges = rows.chunk == 0 || at.i == 0;   // a sequence starts or ends in this tile
+        bool edges = false;   // packed: a sequence starts or ends in this tile
         if (packed) {
             mark_sequences(p, marks, tile0, lo, hi);
             bool f = false;
@@ -861,19 +864,12 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
             edges = __syncthreads_or(f);
         }
         const bool whole = !packed || (tile0 >= lo && tile0 + CHUNK <= hi);   // the tile's rows are all written, or do not exist
-        const bool plain = whole && !edges && tile0 + CHUNK <= p.a.L && (M::ON || rows.mine);
+        // rows that do not exist hold the state and the gradient, and have no values
+        const bool full = tile0 + CHUNK <= p.a.L, plain = whole && !edges && (M::ON || (full && rows.mine));
         auto in = [&](int r) { return r < rows.count && rows.t0 + r >= lo && rows.t0 + r < hi; };
-        // the sequence that row r starts or ends, or -1
-        auto starts = [&](int r) -> long long {
-            if (!rows.mine) return -1;
-            if (packed) return marks.first[group * S::ROWS + r];
-            return rows.t0 + r == 0 ? at.b : -1;
-        };
-        auto ends = [&](int r) -> long long {
-            if (!rows.mine) return -1;
-            if (packed) return marks.last[group * S::ROWS + r];
-            return rows.t0 + r == p.a.L - 1 ? at.b : -1;
-        };
+        // packed: the sequence that row r starts or ends, or -1
+        auto starts = [&](int r) { return rows.mine ? marks.first[group * S::ROWS + r] : -1; };
+        auto ends = [&](int r) { return rows.mine ? marks.last[group * S::ROWS + r] : -1; };
 
         bool arrived = true;
         if (M::ON) arrived = mbar_wait(smem_u32(&bars[turn]), phase, COPY_POLLS * 1000);
@@ -886,7 +882,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
 #pragma unroll
             for (int r = 0; r < S::ROWS; r++) {
                 Pack<TG, GV> g;
-                const bool there = plain || in(r);
+                const bool there = (plain && full) || in(r);
                 if constexpr (M::ON) {
                     if constexpr (HEAD) g.v[0] = g_now[r];
                     else g = load<TG, GV>(reinterpret_cast<const TG *>(pg + M::at_g(r)));
@@ -938,7 +934,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
             fill(E, 0.0f);
 #pragma unroll
             for (int r = 0; r < S::ROWS; r++) {
-                if (CARE && packed && edges) {
+                if (CARE && edges) {
                     const long long n = starts(r);
                     if (n >= 0)
 #pragma unroll
@@ -1047,7 +1043,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
             if (x < S::WIDTH) ahead.state[x] = p.serial ? carry : cx < p.C ? look_near<S::WIDTH>(words + x, at.i) : 0.0f;
             __syncthreads();
         } else {
-            if (x < S::WIDTH) ahead.state[x] = 0.0f;
+            if (x < S::WIDTH) ahead.state[x] = !packed && p.a.dhT && cx < p.C ? p.a.dhT[(long long)at.b * p.C + cx] : 0.0f;
             __syncthreads();
         }
         if (x < S::WIDTH && cx < p.C) {
@@ -1086,7 +1082,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
             float slope[S::ROWS][V];
 #pragma unroll
             for (int r = 0; r < S::ROWS; r++) {
-                if (CARE && packed && edges) {
+                if (CARE && edges) {
                     const long long n = starts(r);
                     if (n >= 0)
 #pragma unroll
@@ -1174,8 +1170,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
             if constexpr (HEAD) {
                 // the sums over a head's lanes
                 auto write = [&](int r, float sum) {
-                    const bool here = !CARE || in(r);
-                    if (!here && !(r < rows.count && p.a.zero_outside)) return;
+                    if (r >= rows.count || (CARE && !in(r) && !p.a.zero_outside)) return;
                     if (!p.parts)
                         dg_row[r * p.a.dg.row_stride] = from_f<TG>(sum);
                     else
@@ -1219,6 +1214,9 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
             finish(std::false_type{});
         else
             finish(std::true_type{});
+        if (!packed && rows.chunk == 0 && group == 0 && rows.mine && p.a.dh0)
+#pragma unroll
+            for (int j = 0; j < V; j++) p.a.dh0[(long long)at.b * p.C + c + j] = e[j];
         if (packed && at.i == 0) pass_empty(p, p.a.dhT, p.a.dh0, c0, S::WIDTH);
         if (M::ON) {
             fence_proxy_async();
@@ -1349,7 +1347,7 @@ Work work_of(const gated_scan_s *h, long long B, long long L, bool backward, int
     // channels take 9.9 us by look back and 8.0 us in one strip's order, 1,024 rows 13.9 and 18.9.
     const long long one = (strips + most - 1) / most * nchunk, all = (strips * nchunk + most - 1) / most;
     Work w{};
-    w.serial = one * 6 <= all * 7 + 12;
+    w.serial = one * 20 <= all * 21 + 20;
     if (!w.serial) w.words = ((size_t)strips * nchunk + AHEAD) * width_of(h, V) * 8;
     w.words = (w.words + 255) / 256 * 256;
     const int pieces = backward ? pieces_of(h, V) : 1;
