@@ -10,6 +10,7 @@ built -- there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 from typing import Optional, Tuple
@@ -500,10 +501,16 @@ def _dtype_code(name: str, what: str) -> int:
     raise ValueError(f"{what} must be 'f32' or 'bf16', not {name!r}")
 
 
-def _torch_dtype(code: int):
+@functools.lru_cache(maxsize=None)
+def _torch():
     import torch
 
-    return torch.float32 if code == SPECTRE_F32 else torch.bfloat16
+    return torch
+
+
+@functools.lru_cache(maxsize=None)
+def _torch_dtype(code: int):
+    return _torch().float32 if code == SPECTRE_F32 else _torch().bfloat16
 
 
 def _check_tensor(name, t, shape, dtype, device):
@@ -578,8 +585,7 @@ def _stream_for(stream, device, tensors) -> int:
     """The raw stream of a call.  Where it is not the current one, the tensors are
     marked as in use on it, so that their memory is not handed out again before
     the work enqueued there is done."""
-    import torch
-
+    torch = _torch()
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device.index)
     current = torch._C._cuda_getCurrentRawStream(device.index)
@@ -625,8 +631,7 @@ def gated_scan_destroy(h: Optional[int]) -> None:
 
 def check_scan_sequences(B, L, cu_seqlens, device=None) -> int:
     """Sequences of a call: B, or those of cu_seqlens (int32 [N + 1], B = 1)."""
-    import torch
-
+    torch = _torch()
     if cu_seqlens is None:
         return B
     if B != 1:
@@ -676,8 +681,7 @@ class GatedScan:
 
     def __init__(self, H: int, D: int, dtype: str = "bf16", gate: str = "sigmoid",
                  gate_per: str = "channel", gate_dtype: Optional[str] = None):
-        import torch
-
+        torch = _torch()
         self.handle = None
         if gate not in GATED_SCAN_GATE or gate_per not in GATED_SCAN_PER:
             raise ValueError("gate must be 'sigmoid' or 'exp', gate_per 'channel' or 'head'")
@@ -691,13 +695,11 @@ class GatedScan:
     def new_states(self, B: int, L: int):
         """The tensor that a training forward fills and backward reads: the fp32 state
         before every GATED_SCAN_CHUNK-th row."""
-        import torch
-
+        torch = _torch()
         return torch.empty((B, -(-L // GATED_SCAN_CHUNK), self.C), dtype=torch.float32, device=self.device)
 
     def _check_states(self, B, L, nseq, states, **ends):
-        import torch
-
+        torch = _torch()
         if states is not None:
             _check_plain("states", states, (B, -(-L // GATED_SCAN_CHUNK), self.C), torch.float32, self.device)
         for name, t in ends.items():
@@ -705,14 +707,12 @@ class GatedScan:
                 _check_plain(name, t, (nseq, self.C), torch.float32, self.device)
 
     def _work(self, B, L, backward):
-        import torch
-
+        torch = _torch()
         n = gated_scan_workspace_bytes(self.handle, B, L, backward)
         return (torch.empty(n, dtype=torch.uint8, device=self.device), n) if n else (None, 0)
 
     def __call__(self, g, v, h0=None, cu_seqlens=None, y=None, hT=None, states=None, stream=None):
-        import torch
-
+        torch = _torch()
         device = self.device
         B, L = check_scan_arguments(self.H, self.D, self.per, self.dtype_code, self.gate_code, g, v, device)
         nseq = B if cu_seqlens is None else check_scan_sequences(B, L, cu_seqlens, device)
@@ -740,8 +740,7 @@ class GatedScan:
         """(dg, dv, dh0) from dy (and dhT, the gradient of the final states); dh0 is None
         where h0 is None and no dh0 is given.  ``states`` is what the forward call with the
         same g, v, h0 and cu_seqlens filled."""
-        import torch
-
+        torch = _torch()
         device = self.device
         B, L = check_scan_arguments(self.H, self.D, self.per, self.dtype_code, self.gate_code, g, v,
                                     device, dy=dy, dg=dg, dv=dv)
@@ -776,8 +775,7 @@ class GatedScan:
         Returns (y, new_state); new_state is the pool itself, updated in place, unless
         another tensor is given (its other rows are left as they are).  A row whose slot is
         outside the pool is skipped: its y is left as it is, or zero where y is made here."""
-        import torch
-
+        torch = _torch()
         device, B, C = self.device, v.shape[0], self.C
         _check_tensor("g", g, (B, self.H if self.per == GATED_SCAN_PER["head"] else C),
                       _torch_dtype(self.gate_code), device)
@@ -848,8 +846,7 @@ def check_norm_arguments(C, dtype_code, device=None, vectors=(), **rows) -> Tupl
     """Shapes and types of a residual norm's tensors: rows [..., C] of the plan's type,
     all of one shape, and ``vectors`` ((name, tensor), ...) of C fp32 values.  Returns
     that shape."""
-    import torch
-
+    torch = _torch()
     shape, dtype = None, _torch_dtype(dtype_code)
     for name, t in rows.items():
         if t is None:
@@ -877,8 +874,7 @@ class ResidualNorm:
     """
 
     def __init__(self, C: int, dtype: str = "bf16", norm: str = "post_ln", eps: float = 1e-5):
-        import torch
-
+        torch = _torch()
         self.handle = None
         if norm not in SPECTRE_NORM:
             raise ValueError(f"norm must be one of {sorted(SPECTRE_NORM)}, not {norm!r}")
@@ -889,23 +885,23 @@ class ResidualNorm:
         self.device = torch.device("cuda", torch.cuda.current_device())
 
     def __call__(self, out, x, gamma, beta, y=None, stream=None):
-        import torch
-
+        torch = _torch()
         check_norm_arguments(self.C, self.dtype_code, self.device, (("gamma", gamma), ("beta", beta)),
                              out=out, x=x, y=y)
+        C = self.C
         if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=self.device)
+            y, y_stride = torch.empty(x.shape, dtype=x.dtype, device=self.device), C
         else:
             _check_outputs([("y", y)], [("out", out), ("x", x)])
+            y_stride = _row_stride("y", y)
         raw = _stream_for(stream, self.device, (out, x, gamma, beta, y))
-        _check(_lib.residual_norm_run(self.handle, x.numel() // self.C, out.data_ptr(), _row_stride("out", out),
+        _check(_lib.residual_norm_run(self.handle, x.numel() // C, out.data_ptr(), _row_stride("out", out),
                                       x.data_ptr(), _row_stride("x", x), gamma.data_ptr(), beta.data_ptr(),
-                                      y.data_ptr(), _row_stride("y", y), raw), "residual_norm_run")
+                                      y.data_ptr(), y_stride, raw), "residual_norm_run")
         return y
 
     def backward(self, dy, out, x, gamma, dout=None, dgamma=None, dbeta=None, stream=None):
-        import torch
-
+        torch = _torch()
         if self.post and x is None:
             raise ValueError("the post forms' gradient needs x")
         check_norm_arguments(self.C, self.dtype_code, self.device,

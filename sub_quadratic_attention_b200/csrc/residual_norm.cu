@@ -371,17 +371,22 @@ __global__ void __maxnreg__((REGISTERS<EPT, true>)) norm_backward(const __grid_c
     }
 }
 
-// column c of the blocks' sums [n][2][C]: the 16 threads of a column take every 16th block
-constexpr int JOIN_COLS = 32, JOIN_ROWS = 16;
+// column c of the blocks' sums [n][2][C]: the JOIN_ROWS threads of a column take every JOIN_ROWS-th
+// block, then their sums are added in order.  Launched ahead of the end of the kernel that it
+// waits for, so that its own start is not added to it.
+constexpr int JOIN_COLS = 32, JOIN_ROWS = 32;
 __global__ void __launch_bounds__(JOIN_COLS *JOIN_ROWS) join_blocks(const float *part, int n, int C, float *dgamma, float *dbeta) {
     __shared__ float sums[JOIN_ROWS][JOIN_COLS];
     const int c = blockIdx.x * JOIN_COLS + threadIdx.x;
+    cudaGridDependencySynchronize();
     float s = 0.0f;
     if (c < 2 * C)
+#pragma unroll 8
         for (int i = threadIdx.y; i < n; i += JOIN_ROWS) s += part[(long long)i * 2 * C + c];
     sums[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.y || c >= 2 * C) return;
+#pragma unroll
     for (int i = 1; i < JOIN_ROWS; i++) s += sums[i][threadIdx.x];
     (c < C ? dgamma[c] : dbeta[c - C]) = s;
 }
@@ -573,8 +578,16 @@ int residual_norm_backward(residual_norm_t h, long long T, const void *dy, long 
         const int st = enqueue(h, a, true, n, s);
         if (st != SPECTRE_OK || n == 1) return st;
     }
-    join_blocks<<<(2 * h->C + JOIN_COLS - 1) / JOIN_COLS, dim3(JOIN_COLS, JOIN_ROWS), 0, s>>>(part, n, h->C, dgamma, dbeta);
-    return status_of(cudaGetLastError());
+    cudaLaunchConfig_t config{};
+    config.gridDim = dim3((2 * h->C + JOIN_COLS - 1) / JOIN_COLS);
+    config.blockDim = dim3(JOIN_COLS, JOIN_ROWS);
+    config.stream = s;
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    config.attrs = &early;
+    config.numAttrs = T > 0 ? 1 : 0;
+    return status_of(cudaLaunchKernelEx(&config, join_blocks, static_cast<const float *>(part), n, h->C, dgamma, dbeta));
 }
 
 int residual_norm_destroy(residual_norm_t h) {
