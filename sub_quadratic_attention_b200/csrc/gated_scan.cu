@@ -324,43 +324,57 @@ template <int WIDTH> __device__ __forceinline__ float look_near(const unsigned l
 template <int WIDTH, int QS>
 __device__ __forceinline__ void look_back(LookBack<WIDTH, QS> &m, const unsigned long long *words, int i, bool mine) {
     const int x = threadIdx.x % WIDTH, q = threadIdx.x / WIDTH;
+    // words ahead of tile 0 belong to others, or to nobody: tile 0's comes before them
+    const unsigned long long *from = words + (long long)(i - 1 - q * REACH) * WIDTH + x;
     unsigned long long w[REACH];
-    for (unsigned polls = 0;; polls++) {
-        {
-            // words ahead of tile 0 belong to others, or to nobody: tile 0's comes before them
-            const unsigned long long *from = words + (long long)(i - 1 - q * REACH) * WIDTH + x;
 #pragma unroll
-            for (int j = 0; j < REACH; j++) w[j] = peek(from - j * WIDTH);
-            int seen = REACH;       // how many pairs come before a word with P = 0; one more: a word is missing
+    for (int j = 0; j < REACH; j++) w[j] = peek(from - j * WIDTH);
+    unsigned polls = 0;
+    for (bool found = false; !found;) {
+        // each thread by itself until its words are there, up to one with P = 0
+        int seen;
+        for (;; polls++) {
+            seen = REACH;       // how many pairs come before a word with P = 0; one more: a word is missing
 #pragma unroll
             for (int j = REACH - 1; j >= 0; j--) {
                 const unsigned P = (unsigned)(w[j] >> 32);
                 seen = P == (unsigned)(NOTHING >> 32) ? REACH + 1 : P == 0 ? j : seen;
             }
-            if (!mine) seen = 0;
-            m.seen[q][x] = (unsigned char)seen;
+            if (!mine || i - 1 - q * REACH < 0) seen = 0;
+            if (seen <= REACH || polls >= MOST_POLLS) break;
+            // the others are good as they are: a pair that became a state meanwhile says the same
+#pragma unroll
+            for (int j = 0; j < REACH; j++)
+                if (w[j] == NOTHING) w[j] = peek(from - j * WIDTH);
         }
+        m.seen[q][x] = (unsigned char)seen;
         __syncthreads();
-        int from = 0, at = REACH;   // the word with P = 0: thread from's number at
-        while (from < QS && (at = m.seen[from][x]) == REACH) from++;
-        if (__syncthreads_or(at >= REACH)) {
-            if (polls < MOST_POLLS) continue;
-            if (q == 0) m.state[x] = __uint_as_float(0x7fc00000u);
-            __syncthreads();
-            return;
+        int nearest = 0, at = REACH;   // the word with P = 0: thread nearest's number at
+        while (nearest < QS && (at = m.seen[nearest][x]) == REACH) nearest++;
+        found = !__syncthreads_or(at >= REACH);
+        if (!found) {
+            if (__syncthreads_or(++polls >= MOST_POLLS)) {
+                if (q == 0) m.state[x] = __uint_as_float(0x7fc00000u);
+                __syncthreads();
+                return;
+            }
+            // pairs alone: the farthest of them become states first
+            if (q == QS - 1)
+#pragma unroll
+                for (int j = 0; j < REACH; j++) w[j] = peek(from - j * WIDTH);
+            continue;
         }
         // from the farthest word on, in order
-        for (int k = __syncthreads_or(from > 0) ? QS - 1 : 0; k >= 0; k--) {
-            if (q == k && k <= from) {
-                float state = k == from ? 0.0f : m.state[x];
+        for (int k = __syncthreads_or(nearest > 0) ? QS - 1 : 0; k >= 0; k--) {
+            if (q == k && k <= nearest) {
+                float state = k == nearest ? 0.0f : m.state[x];
 #pragma unroll
                 for (int j = REACH - 1; j >= 0; j--)
-                    if (k < from || j <= at) state = fma0(word_P(w[j]), state, word_Q(w[j]));
+                    if (k < nearest || j <= at) state = fma0(word_P(w[j]), state, word_Q(w[j]));
                 m.state[x] = mine ? state : 0.0f;
             }
             __syncthreads();
         }
-        return;
     }
 }
 
