@@ -42,7 +42,9 @@
  *
  * Ownership: the caller owns every tensor and the workspace; the handle holds no
  * device memory and is not changed by a run, so one handle may be used on several
- * streams and threads at once, each call with a workspace of its own.
+ * streams and threads at once, each call with a workspace of its own.  Long sequences
+ * of few channels are one cooperative launch: its blocks start together, when the
+ * device has room for all of them.
  *
  * Errors: the spectre_status codes of spectre_mix.h; no function throws or exits.
  */
@@ -113,6 +115,7 @@ int gated_scan_run(gated_scan_t h, const gated_scan_args *a, void *stream);
 /*
  * Enqueue the backward pass: reads dy, g, v, h0, dhT and the states that
  * gated_scan_run wrote for the same inputs; writes dg, dv and, where given, dh0.
+ * L = 0 sets dh0 to dhT (or 0).
  *   dh_t = dy_t + a_{t+1} dh_{t+1};  dh0 = a_0 dh_0
  *   sigmoid: dv = dh (1 - a), dg = dh (h_{t-1} - v) a (1 - a);
  *   exp:     dv = dh,         dg = dh h_{t-1} a
@@ -127,13 +130,23 @@ int gated_scan_backward(gated_scan_t h, const gated_scan_args *a, void *stream);
  *               place) and may not overlap it otherwise.  Pool rows that no slot names
  *               are left as they are.
  *   slots     : [B] int32 (device), or NULL: row i has slot i, and S >= B.
- *               A row whose slot is outside [0, S) is skipped: its y is left as it is.
+ *               A row whose slot is outside [0, S) is skipped: its y is left as it is, or
+ *               set to zero with zero_skipped.
  *               Rows that name the same slot are taken in order, one after another.
  */
 int gated_scan_step(gated_scan_t h, long long B, const void *g, long long g_stride,
                     const void *v, long long v_stride, const float *state, long long S,
                     const int *slots, void *y, long long y_stride, float *new_state,
-                    void *stream);
+                    int zero_skipped, void *stream);
+
+/*
+ * Synchronise `stream` and report device-side failures of earlier gated scans on the
+ * handle's device: SPECTRE_ERR_TIMEOUT if a bounded wait (for a copy, or for the state
+ * ahead of a block of rows) gave up in any run since the last call, else SPECTRE_OK.
+ * Clears the record.  A wait that gives up, after some seconds, leaves NaN in the rows
+ * behind it, so the failure shows in the output as well.
+ */
+int gated_scan_device_status(gated_scan_t h, void *stream);
 
 /* Release the handle.  NULL-safe; returns SPECTRE_OK. */
 int gated_scan_destroy(gated_scan_t h);

@@ -66,6 +66,11 @@ int residual_norm_backward(residual_norm_t h, long long T, const void *dy, long 
                            float *dgamma, float *dbeta, void *work, size_t work_bytes,
                            void *stream);
 
+/* Synchronise `stream`; SPECTRE_ERR_TIMEOUT if a bounded wait for a copy gave up in any
+ * residual norm on the handle's device since the last call (its row is NaN), else
+ * SPECTRE_OK.  Clears the record. */
+int residual_norm_device_status(residual_norm_t h, void *stream);
+
 /* Release the handle.  NULL-safe; returns SPECTRE_OK. */
 int residual_norm_destroy(residual_norm_t h);
 

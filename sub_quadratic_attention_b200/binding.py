@@ -80,13 +80,15 @@ SIGNATURES = {
     "gated_scan_workspace_bytes": (_sz, [_vp, _ll, _ll, _i]),
     "gated_scan_run": (_i, [_vp, ctypes.c_char_p, _vp]),
     "gated_scan_backward": (_i, [_vp, ctypes.c_char_p, _vp]),
-    "gated_scan_step": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _ll, _vp, _vp]),
+    "gated_scan_step": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _ll, _vp, _i, _vp]),
+    "gated_scan_device_status": (_i, [_vp, _vp]),
     "gated_scan_destroy": (_i, [_vp]),
     "residual_norm_create": (_i, [ctypes.POINTER(_vp), _i, _i, _i, ctypes.c_float]),
     "residual_norm_run": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _ll, _vp]),
     "residual_norm_workspace_bytes": (_sz, [_vp, _ll]),
     "residual_norm_backward": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _ll, _vp, _vp,
                                     _vp, _sz, _vp]),
+    "residual_norm_device_status": (_i, [_vp, _vp]),
     "residual_norm_destroy": (_i, [_vp]),
 }
 
@@ -625,6 +627,11 @@ def gated_scan_backward(h: int, args: bytes, stream: int) -> None:
     _check(_lib.gated_scan_backward(h, args, stream), "gated_scan_backward")
 
 
+def gated_scan_device_status(h: int, stream=None) -> int:
+    """Synchronise and return SPECTRE_OK or SPECTRE_ERR_TIMEOUT for earlier scans."""
+    return _lib.gated_scan_device_status(h, _stream(stream))
+
+
 def gated_scan_destroy(h: Optional[int]) -> None:
     _check(_lib.gated_scan_destroy(h), "gated_scan_destroy")
 
@@ -790,8 +797,9 @@ class GatedScan:
             _check_plain("slots", slots, (B,), torch.int32, device)
         elif S < B:
             raise ValueError(f"state holds {S} rows, the step has {B}")
-        if y is None:
-            y = (torch.empty if slots is None else torch.zeros)((B, C), dtype=v.dtype, device=device)
+        made = y is None
+        if made:
+            y = torch.empty((B, C), dtype=v.dtype, device=device)
         else:
             _check_tensor("y", y, (B, C), v.dtype, device)
             _check_outputs([("y", y)], [("g", g), ("v", v), ("state", state), ("new_state", new_state)])
@@ -801,7 +809,7 @@ class GatedScan:
         raw = _stream_for(stream, device, (g, v, state, slots, y, new_state))
         _check(_lib.gated_scan_step(self.handle, B, g.data_ptr(), gs, v.data_ptr(), vs, state.data_ptr(), S,
                                     None if slots is None else slots.data_ptr(), y.data_ptr(), ys,
-                                    new_state.data_ptr(), raw), "gated_scan_step")
+                                    new_state.data_ptr(), made, raw), "gated_scan_step")
         return y, new_state
 
     def close(self) -> None:
@@ -836,6 +844,11 @@ def residual_norm_create(C: int, dtype: int, norm: int, eps: float = 1e-5) -> in
 
 def residual_norm_workspace_bytes(h: Optional[int], T: int) -> int:
     return int(_lib.residual_norm_workspace_bytes(h, T))
+
+
+def residual_norm_device_status(h: int, stream=None) -> int:
+    """Synchronise and return SPECTRE_OK or SPECTRE_ERR_TIMEOUT for earlier norms."""
+    return _lib.residual_norm_device_status(h, _stream(stream))
 
 
 def residual_norm_destroy(h: Optional[int]) -> None:

@@ -246,6 +246,9 @@ template <typename TV, int V> struct Tile {
 constexpr unsigned long long NOTHING = ~0ull;
 constexpr unsigned MOST_POLLS = 1u << 22;   // of about a microsecond each
 
+// Set where a bounded wait gave up; gated_scan_device_status reads and clears it.
+__device__ unsigned wait_gave_up;
+
 struct Args {
     gated_scan_args a;
     int H, D, C;
@@ -299,6 +302,10 @@ template <int WIDTH, int QS> struct alignas(16) LookBack {
     float state[WIDTH];
     unsigned char seen[QS][WIDTH];
 };
+__device__ __forceinline__ float gave_up() {
+    atomicExch(&wait_gave_up, 1u);
+    return __uint_as_float(0x7fc00000u);
+}
 // The same for one channel by one thread, where few tiles are in flight.
 template <int WIDTH> __device__ __forceinline__ float look_near(const unsigned long long *words, int i) {
     const unsigned long long *from = words + (long long)(i - 1) * WIDTH;
@@ -319,7 +326,7 @@ template <int WIDTH> __device__ __forceinline__ float look_near(const unsigned l
             if (j <= seen) state = fma0(word_P(w[j]), state, word_Q(w[j]));
         return state;
     }
-    return __uint_as_float(0x7fc00000u);
+    return gave_up();
 }
 template <int WIDTH, int QS>
 __device__ __forceinline__ void look_back(LookBack<WIDTH, QS> &m, const unsigned long long *words, int i, bool mine) {
@@ -354,7 +361,7 @@ __device__ __forceinline__ void look_back(LookBack<WIDTH, QS> &m, const unsigned
         found = !__syncthreads_or(at >= REACH);
         if (!found) {
             if (__syncthreads_or(++polls >= MOST_POLLS)) {
-                if (q == 0) m.state[x] = __uint_as_float(0x7fc00000u);
+                if (q == 0) m.state[x] = gave_up();
                 __syncthreads();
                 return;
             }
@@ -524,7 +531,7 @@ template <typename TV, typename TG, bool HEAD, int V> struct Rows {
 
 // Blocks an SM.
 template <typename TV, bool HEAD> constexpr int FORWARD_BLOCKS = HEAD && sizeof(TV) == 4 ? 5 : 3;
-constexpr int SINGLE_BLOCKS = 2;   // channels one by one
+constexpr int SINGLE_BLOCKS = 3;   // channels one by one, in either direction
 
 template <typename TV, typename TG, int FORM, bool HEAD, int V>
 __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS : FORWARD_BLOCKS<TV, HEAD>)
@@ -692,7 +699,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
 #pragma unroll
             for (int j = 0; j < V; j++) {
                 lp[j] = lastP[HEAD ? 0 : j];
-                lq[j] = arrived ? Q[S::ROWS - 1][j] : __uint_as_float(0x7fc00000u);
+                lq[j] = arrived ? Q[S::ROWS - 1][j] : gave_up();
             }
             put(&sP[group][lane * V], lp);
             put(&sQ[group][lane * V], lq);
@@ -808,7 +815,7 @@ __host__ __device__ __forceinline__ int last_strip(int h, int D, int width) { re
 constexpr int BACKWARD_BLOCKS = 2;   // an SM: 128 registers a thread, 111 KB of shared memory
 
 template <typename TV, typename TG, int FORM, bool HEAD, int V>
-__global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
+__global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS : BACKWARD_BLOCKS)
     scan_backward(const __grid_constant__ Args p, const __grid_constant__ Maps maps) {
     using S = Tile<TV, V>;
     using M = Stage<TV, TG, HEAD, V>;
@@ -997,7 +1004,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, BACKWARD_BLOCKS)
         }
         if (!fine) walk(std::true_type{});
 #pragma unroll
-        for (int j = 0; j < V; j++) E[j] = arrived ? E[j] : __uint_as_float(0x7fc00000u);
+        for (int j = 0; j < V; j++) E[j] = arrived ? E[j] : gave_up();
         put(&sQ[group][lane * V], Q);
         put(&sR[group][lane * V], T);
         put(&sE[group][lane * V], E);
@@ -1267,7 +1274,8 @@ template <typename TG> __global__ void join_parts(Args p, int width) {
 constexpr int STEP_THREADS = 128;
 template <typename TV, typename TG, int FORM, bool HEAD, int V>
 __global__ void __launch_bounds__(STEP_THREADS) scan_step(int B, int C, int D, const TG *g, long long gs, const TV *v, long long vs,
-                                                          const float *state, long long S, const int *slots, TV *y, long long ys, float *next) {
+                                                          const float *state, long long S, const int *slots, TV *y, long long ys, float *next,
+                                                          int zero_skipped) {
     constexpr int GV = HEAD ? 1 : V;
     const int c = (blockIdx.y * STEP_THREADS + threadIdx.x) * V, i0 = blockIdx.x;
     const int gc = HEAD ? c / D : c;
@@ -1286,10 +1294,15 @@ __global__ void __launch_bounds__(STEP_THREADS) scan_step(int B, int C, int D, c
         bool before = false;
         for (int j = threadIdx.x; j < B; j += STEP_THREADS)
             if (j != i0 && slots[j] == slot) (j < i0 ? before : behind) = true;
-        if (__syncthreads_or(before)) return;
+        if (__syncthreads_or(before && there)) return;
         behind = __syncthreads_or(behind);
     }
-    if (!there || c >= C) return;
+    if (c >= C) return;
+    if (!there) {
+        const float zero[V] = {};
+        if (zero_skipped) store<TV, V>(y + i0 * ys + c, zero);
+        return;
+    }
     for (int i = i0;;) {
         float f[V];
 #pragma unroll
@@ -1342,8 +1355,8 @@ int pieces_of(const gated_scan_s *h, int V) {
 
 // Blocks an SM that the kernels are built for.
 int blocks_per_sm(const gated_scan_s *h, bool backward, int V) {
-    if (backward) return BACKWARD_BLOCKS;
     if (V == 1) return SINGLE_BLOCKS;
+    if (backward) return BACKWARD_BLOCKS;
     const bool head = h->per == GATED_SCAN_PER_HEAD;
     return h->dtype == SPECTRE_F32 ? (head ? FORWARD_BLOCKS<float, true> : FORWARD_BLOCKS<float, false>)
                                    : (head ? FORWARD_BLOCKS<__nv_bfloat16, true> : FORWARD_BLOCKS<__nv_bfloat16, false>);
@@ -1554,10 +1567,11 @@ int run(gated_scan_s *h, const gated_scan_args *a, bool backward, void *stream) 
 
 template <typename TV, typename TG, int FORM, bool HEAD, int V>
 cudaError_t launch_step(const gated_scan_s *h, long long B, const void *g, long long gs, const void *v, long long vs,
-                        const float *state, long long S, const int *slots, void *y, long long ys, float *next, cudaStream_t s) {
+                        const float *state, long long S, const int *slots, void *y, long long ys, float *next, int zero_skipped,
+                        cudaStream_t s) {
     const dim3 grid((unsigned)B, (h->C + STEP_THREADS * V - 1) / (STEP_THREADS * V));
     scan_step<TV, TG, FORM, HEAD, V><<<grid, STEP_THREADS, 0, s>>>((int)B, h->C, h->D, static_cast<const TG *>(g), gs, static_cast<const TV *>(v), vs,
-                                                                   state, S, slots, static_cast<TV *>(y), ys, next);
+                                                                   state, S, slots, static_cast<TV *>(y), ys, next, zero_skipped);
     return cudaGetLastError();
 }
 
@@ -1596,7 +1610,7 @@ int gated_scan_backward(gated_scan_t h, const gated_scan_args *a, void *stream) 
 
 int gated_scan_step(gated_scan_t h, long long B, const void *g, long long g_stride, const void *v,
                     long long v_stride, const float *state, long long S, const int *slots, void *y,
-                    long long y_stride, float *new_state, void *stream) {
+                    long long y_stride, float *new_state, int zero_skipped, void *stream) {
     using namespace gscan;
     if (!h || B < 0 || S < 0) return SPECTRE_ERR_ARG;
     if (B == 0) return SPECTRE_OK;
@@ -1616,7 +1630,7 @@ int gated_scan_step(gated_scan_t h, long long B, const void *g, long long g_stri
                      aligned(state, 16) && aligned(new_state, 16);
     auto go = [&](auto tv, auto tg, auto form, auto hd, auto four) {
         return status_of(launch_step<decltype(tv), decltype(tg), decltype(form)::value, decltype(hd)::value, decltype(four)::value>(
-            h, B, g, g_stride, v, v_stride, state, S, slots, y, y_stride, new_state, s));
+            h, B, g, g_stride, v, v_stride, state, S, slots, y, y_stride, new_state, zero_skipped, s));
     };
     auto go_shape = [&](auto tv, auto tg, auto form) {
         using one = std::integral_constant<int, 1>;
@@ -1630,6 +1644,17 @@ int gated_scan_step(gated_scan_t h, long long B, const void *g, long long g_stri
         return go_shape(bf(), bf(), form);
     };
     return h->gate == GATED_SCAN_EXP ? go_types(std::integral_constant<int, GATED_SCAN_EXP>{}) : go_types(std::integral_constant<int, GATED_SCAN_SIGMOID>{});
+}
+
+int gated_scan_device_status(gated_scan_t h, void *stream) {
+    if (!h) return SPECTRE_ERR_ARG;
+    if (!gscan::current_device_is(h->device)) return SPECTRE_ERR_DEVICE;
+    unsigned word = 0;
+    const unsigned clear = 0;
+    cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&word, gscan::wait_gave_up, sizeof word);
+    if (e == cudaSuccess && word) e = cudaMemcpyToSymbol(gscan::wait_gave_up, &clear, sizeof clear);
+    return e == cudaSuccess && word ? SPECTRE_ERR_TIMEOUT : rows_io::status_of(e);
 }
 
 int gated_scan_destroy(gated_scan_t h) {

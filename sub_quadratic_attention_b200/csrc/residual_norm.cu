@@ -120,6 +120,9 @@ template <int K> __device__ __forceinline__ void row_sums(float (&s)[K], int tpr
     turn ^= 1;
 }
 
+// Set where a bounded wait gave up; residual_norm_device_status reads and clears it.
+__device__ unsigned wait_gave_up;
+
 using spectre::tc::bulk_copy_g2s;
 using spectre::tc::mbar_arrive_expect_tx;
 using spectre::tc::mbar_init;
@@ -175,6 +178,7 @@ template <typename T, int VEC, int EPT, int N, bool RING> struct Part {
     template <typename M> __device__ __forceinline__ bool fetch(bool there, const M &mine, int c, int apart) {
         bool came = true;
         if (RING && there) came = mbar_wait(bars + 8 * stage, phase, COPY_POLLS);
+        if (!came) atomicExch(&wait_gave_up, 1u);
 #pragma unroll
         for (int k = 0; k < N; k++) {
 #pragma unroll
@@ -588,6 +592,17 @@ int residual_norm_backward(residual_norm_t h, long long T, const void *dy, long 
     config.attrs = &early;
     config.numAttrs = T > 0 ? 1 : 0;
     return status_of(cudaLaunchKernelEx(&config, join_blocks, static_cast<const float *>(part), n, h->C, dgamma, dbeta));
+}
+
+int residual_norm_device_status(residual_norm_t h, void *stream) {
+    if (!h) return SPECTRE_ERR_ARG;
+    if (!resnorm::current_device_is(h->device)) return SPECTRE_ERR_DEVICE;
+    unsigned word = 0;
+    const unsigned clear = 0;
+    cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&word, resnorm::wait_gave_up, sizeof word);
+    if (e == cudaSuccess && word) e = cudaMemcpyToSymbol(resnorm::wait_gave_up, &clear, sizeof clear);
+    return e == cudaSuccess && word ? SPECTRE_ERR_TIMEOUT : rows_io::status_of(e);
 }
 
 int residual_norm_destroy(residual_norm_t h) {

@@ -384,6 +384,7 @@ def test_equal_inputs_give_equal_bits():
             st = s.new_states(1, 40000)
             out = s(g, v, states=st)
             runs.append([*out, st, *s.backward(dy, g, v, st)[:2]])
+        assert b.gated_scan_device_status(s.handle) == b.SPECTRE_OK
     for other in runs[1:]:
         assert all(torch.equal(x, y) for x, y in zip(runs[0], other))
 

@@ -29,6 +29,7 @@ def _check(form, dtype, out, x, dy, gamma, beta, place=lambda t: t):
         dout, dx, dgamma, dbeta = n.backward(d, o, xx, gamma.cuda())
         again = n.backward(d, o, xx, gamma.cuda())
         torch.cuda.synchronize()
+        assert b.residual_norm_device_status(n.handle) == b.SPECTRE_OK
     assert dx is (dout if form.startswith("post") else d)
     for p, q in zip((dout, dgamma, dbeta), (again[0], again[2], again[3])):
         assert torch.equal(p.view(torch.uint8), q.view(torch.uint8))

@@ -70,7 +70,8 @@ def test_null_handles():
     a = b.gated_scan_args(1, 1, (0, 0, 0), (0, 0, 0))
     assert b._lib.gated_scan_run(None, a, None) == b.SPECTRE_ERR_ARG
     assert b._lib.gated_scan_backward(None, a, None) == b.SPECTRE_ERR_ARG
-    assert b._lib.gated_scan_step(None, 1, None, 0, None, 0, None, 0, None, None, 0, None, None) == b.SPECTRE_ERR_ARG
+    assert b._lib.gated_scan_step(None, 1, None, 0, None, 0, None, 0, None, None, 0, None, 0, None) == b.SPECTRE_ERR_ARG
+    assert b._lib.gated_scan_device_status(None, None) == b._lib.residual_norm_device_status(None, None) == b.SPECTRE_ERR_ARG
     assert b.gated_scan_workspace_bytes(None, 1, 1, True) == 0
     assert b._lib.residual_norm_run(None, 1, None, 0, None, 0, None, None, None, 0, None) == b.SPECTRE_ERR_ARG
     assert b._lib.residual_norm_backward(None, 1, None, 0, None, 0, None, 0, None, None, 0, None, None, None, 0,
