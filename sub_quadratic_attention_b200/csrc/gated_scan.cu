@@ -334,13 +334,13 @@ __device__ __forceinline__ void look_back(LookBack<WIDTH, QS> &m, const unsigned
     // words ahead of tile 0 belong to others, or to nobody: tile 0's comes before them
     const unsigned long long *from = words + (long long)(i - 1 - q * REACH) * WIDTH + x;
     unsigned long long w[REACH];
-#pragma unroll
-    for (int j = 0; j < REACH; j++) w[j] = peek(from - j * WIDTH);
     unsigned polls = 0;
     for (bool found = false; !found;) {
         // each thread by itself until its words are there, up to one with P = 0
         int seen;
-        for (;; polls++) {
+        do {
+#pragma unroll
+            for (int j = 0; j < REACH; j++) w[j] = peek(from - j * WIDTH);
             seen = REACH;       // how many pairs come before a word with P = 0; one more: a word is missing
 #pragma unroll
             for (int j = REACH - 1; j >= 0; j--) {
@@ -348,12 +348,7 @@ __device__ __forceinline__ void look_back(LookBack<WIDTH, QS> &m, const unsigned
                 seen = P == (unsigned)(NOTHING >> 32) ? REACH + 1 : P == 0 ? j : seen;
             }
             if (!mine || i - 1 - q * REACH < 0) seen = 0;
-            if (seen <= REACH || polls >= MOST_POLLS) break;
-            // the others are good as they are: a pair that became a state meanwhile says the same
-#pragma unroll
-            for (int j = 0; j < REACH; j++)
-                if (w[j] == NOTHING) w[j] = peek(from - j * WIDTH);
-        }
+        } while (seen > REACH && ++polls < MOST_POLLS);
         m.seen[q][x] = (unsigned char)seen;
         __syncthreads();
         int nearest = 0, at = REACH;   // the word with P = 0: thread nearest's number at
@@ -365,10 +360,6 @@ __device__ __forceinline__ void look_back(LookBack<WIDTH, QS> &m, const unsigned
                 __syncthreads();
                 return;
             }
-            // pairs alone: the farthest of them become states first
-            if (q == QS - 1)
-#pragma unroll
-                for (int j = 0; j < REACH; j++) w[j] = peek(from - j * WIDTH);
             continue;
         }
         // from the farthest word on, in order
@@ -552,7 +543,9 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
     const int lane = threadIdx.x % S::LANES, group = threadIdx.x / S::LANES;
     Place next(p, blockIdx.x);
     const Place by(p, gridDim.x);
-    // more tiles of a strip in flight than one thread's REACH: ask far at once
+    // more tiles of a strip in flight than one thread's REACH: the whole block looks back.  Where
+    // few are, one thread a channel is enough and asks for less: 64 x 1,024 rows of 512 channels
+    // 51 against 54 us, 4 x 12,288 of 2,048 127 against 137
     const bool far = !p.serial && (unsigned)(p.a.B * p.strips) * REACH < gridDim.x;
     float carry = 0.0f;   // serial: a channel's state (or gradient) behind the last tile
 
@@ -1369,9 +1362,10 @@ struct Work {
 Work work_of(const gated_scan_s *h, long long B, long long L, bool backward, int V) {
     const long long nchunk = (L + CHUNK - 1) / CHUNK, strips = B * strips_of(h, V);
     const long long most = (long long)h->nsm * blocks_per_sm(h, backward, V);
-    // In tiles that the busiest block takes.  Looking back costs each tile about a sixth more and
-    // the launch about two tiles (the words to clear, the blocks to start together): 256 rows of 16
-    // channels take 9.9 us by look back and 8.0 us in one strip's order, 1,024 rows 13.9 and 18.9.
+    // In tiles that the busiest block takes; looking back costs about a twentieth more and, with the
+    // words to clear and the blocks to start together, one tile.  Forward in microseconds, strip by
+    // strip against looking back, rows of 512 bf16 channels: 256 rows 8.2 and 10.3, 1,024 rows 20.5
+    // and 10.3, 111 x 1,024 rows 67 and 79; 4 x 12,288 rows of 2,048 channels 197 and 127.
     const long long one = (strips + most - 1) / most * nchunk, all = (strips * nchunk + most - 1) / most;
     Work w{};
     w.serial = one * 20 <= all * 21 + 20;

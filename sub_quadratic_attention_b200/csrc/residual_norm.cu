@@ -3,10 +3,10 @@
 //
 // TPR threads (a power of two) hold one row in registers, EPT = 8 or 16 values a thread, so a
 // row is read once: the sums of a row are shuffles within a warp and, for rows wider than a
-// warp's share, one exchange of the warps' sums through shared memory.  Rows come by bulk
-// copies into a ring of stages that each row's threads have for themselves, so that the next
-// rows are on their way without a register while this one is worked on; rows that cannot be
-// copied so (short, or not 16-byte aligned) are loaded by the threads.  The variance is
+// warp's share, one exchange of the warps' sums through shared memory.  Going forward a thread
+// loads its part of the next row before it works on this one.  In the backward pass, which has
+// no registers for that, rows come by bulk copies into a ring of stages that each row's threads
+// have for themselves; rows that cannot be copied so (short, or not 16-byte aligned) are loaded.  The variance is
 // taken about the mean in a second sum over the registers (a one-pass sum of squares loses
 // it where the mean is large).  The backward pass recomputes the row's statistics from its
 // registers instead of reading saved ones, and takes the three sums that need the mean (of
@@ -221,10 +221,8 @@ template <int EPT, bool BACK> constexpr int REGISTERS = BACK ? (EPT == 8 ? 80 : 
 // The next row is loaded ahead where it has no ring and costs at most 32 bytes a tensor and thread.
 template <typename T, int EPT, bool RING> constexpr bool AHEAD = !RING && sizeof(T) * EPT <= 32;
 
-template <typename T, int VEC, int EPT, bool RING, bool FULL, bool LN, bool POST>
+template <typename T, int VEC, int EPT, bool FULL, bool LN, bool POST>
 __global__ void __maxnreg__((REGISTERS<EPT, false>)) norm_forward(const __grid_constant__ Args a) {
-    extern __shared__ __align__(128) char buffers[];
-    __shared__ __align__(8) unsigned long long bars[RING ? MAX_RINGS * MAX_STAGES : 1];
     constexpr int NV = EPT / VEC;
     const int lane = threadIdx.x % a.tpr, group = threadIdx.x / a.tpr, groups = blockDim.x / a.tpr;
     const int c0 = lane * VEC, apart = a.tpr * VEC;
@@ -233,16 +231,14 @@ __global__ void __maxnreg__((REGISTERS<EPT, false>)) norm_forward(const __grid_c
     long long r = blockIdx.x * (long long)groups + group;
     const Mine<NV, FULL> mine(c0, apart, a.C);
     int turn = 0;
-    Part<T, VEC, EPT, 2, RING> next;
+    Part<T, VEC, EPT, 2, false> next;
     next.begin(0, a.out, a.outs, r, rows, c0);
     next.begin(1, a.x, a.xs, r, rows, c0);
     T *y = static_cast<T *>(a.y) + r * a.ys + c0;
-    next.open(a, buffers, bars, group, lane, r, rows);
-    constexpr bool EARLY = AHEAD<T, EPT, RING>;
+    constexpr bool EARLY = AHEAD<T, EPT, false>;
     if (EARLY) next.fetch(r < a.T, mine, c0, apart);
     for (long long r0 = blockIdx.x * (long long)groups; r0 < a.T; r0 += rows, r += rows, y += rows * a.ys) {
-        bool came = true;
-        if (!EARLY) came = next.fetch(r < a.T, mine, c0, apart);
+        if (!EARLY) next.fetch(r < a.T, mine, c0, apart);
         Vec<VEC> z[NV], sums(0.0f), squares(0.0f);
         Pack<T, VEC> xr[POST ? 1 : NV];
 #pragma unroll
@@ -267,8 +263,7 @@ __global__ void __maxnreg__((REGISTERS<EPT, false>)) norm_forward(const __grid_c
             }
         float s[1] = {sum_of(squares)};
         row_sums(s, a.tpr, turn);
-        next.pass(r + next.stages * rows < a.T);
-        const float rstd = came ? rsqrtf(s[0] * inv + a.eps) : __uint_as_float(0x7fc00000u);   // within two units of the last place
+        const float rstd = rsqrtf(s[0] * inv + a.eps);   // within two units of the last place
         const Vec<VEC> scale(rstd);
 #pragma unroll
         for (int i = 0; i < NV; i++) {
@@ -423,9 +418,9 @@ long long backward_blocks(const residual_norm_s *h, long long T) {
 }
 
 template <typename T, int VEC, int EPT, bool RING, bool FULL, bool LN, bool POST>
-cudaError_t launch_rows(const Args &a, bool backward, int grid, cudaStream_t s) {
+cudaError_t launch_backward(const Args &a, int grid, cudaStream_t s) {
     const int threads = block_threads(a.tpr), bytes = RING ? threads / a.tpr * a.stages * a.stage_bytes : 0;
-    const auto kernel = backward ? norm_backward<T, VEC, EPT, RING, FULL, LN, POST> : norm_forward<T, VEC, EPT, RING, FULL, LN, POST>;
+    const auto kernel = norm_backward<T, VEC, EPT, RING, FULL, LN, POST>;
     if (RING) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
@@ -434,15 +429,25 @@ cudaError_t launch_rows(const Args &a, bool backward, int grid, cudaStream_t s) 
     return cudaGetLastError();
 }
 
+template <typename T, int VEC, int EPT, bool LN, bool POST>
+cudaError_t launch_rows(const Args &a, bool backward, int grid, cudaStream_t s) {
+    const bool full = VEC > 1 && a.C == a.tpr * EPT;
+    if (!backward) {
+        if (full)
+            norm_forward<T, VEC, EPT, true, LN, POST><<<grid, block_threads(a.tpr), 0, s>>>(a);
+        else
+            norm_forward<T, VEC, EPT, false, LN, POST><<<grid, block_threads(a.tpr), 0, s>>>(a);
+        return cudaGetLastError();
+    }
+    if constexpr (VEC > 1)
+        if (a.stages)
+            return full ? launch_backward<T, VEC, EPT, true, true, LN, POST>(a, grid, s) : launch_backward<T, VEC, EPT, true, false, LN, POST>(a, grid, s);
+    return launch_backward<T, VEC, EPT, false, false, LN, POST>(a, grid, s);
+}
+
 template <typename T, int VEC, bool LN, bool POST> cudaError_t launch(const Args &a, bool backward, int grid, cudaStream_t s) {
     const bool eight = values_per_thread(a.C, sizeof(T) == 4 ? SPECTRE_F32 : SPECTRE_BF16, backward) == 8;
-    if constexpr (VEC > 1)
-        if (a.stages) {
-            if (a.C == a.tpr * (eight ? 8 : 16))
-                return eight ? launch_rows<T, VEC, 8, true, true, LN, POST>(a, backward, grid, s) : launch_rows<T, VEC, 16, true, true, LN, POST>(a, backward, grid, s);
-            return eight ? launch_rows<T, VEC, 8, true, false, LN, POST>(a, backward, grid, s) : launch_rows<T, VEC, 16, true, false, LN, POST>(a, backward, grid, s);
-        }
-    return eight ? launch_rows<T, VEC, 8, false, false, LN, POST>(a, backward, grid, s) : launch_rows<T, VEC, 16, false, false, LN, POST>(a, backward, grid, s);
+    return eight ? launch_rows<T, VEC, 8, LN, POST>(a, backward, grid, s) : launch_rows<T, VEC, 16, LN, POST>(a, backward, grid, s);
 }
 
 template <typename T, int VEC> cudaError_t launch_norm(int norm, const Args &a, bool backward, int grid, cudaStream_t s) {
@@ -463,10 +468,13 @@ int enqueue(const residual_norm_s *h, Args &a, bool backward, int grid, cudaStre
     const size_t es = h->dtype == SPECTRE_F32 ? 4 : 2;
     const bool vec = (h->C * es) % 16 == 0 && wide(a.out, a.outs, es) && wide(a.x, a.xs, es) && wide(a.y, a.ys, es) &&
                      wide(a.dy, a.dys, es) && aligned(a.gamma, 16) && aligned(a.beta, 16);
-    // rings: rows of a warp or more, each stage one row of every input; four stages where they fit
+    // The backward pass's rings: rows of a warp or more, each stage one row of every input; four stages
+    // where they fit.  Loads instead of rings: 65,536 x 512 bf16 69 against 63 us, 49,152 x 2,048 221
+    // against 198.  Going forward it is the other way: 33 against 39 us and 112 against 125, for a
+    // thread has registers left for the next row and needs no barrier to take it.
     a.stages = 0;
-    if (vec && a.tpr >= 32) {
-        const int inputs = backward ? (a.x ? 3 : 2) : 2, rings = block_threads(a.tpr) / a.tpr;
+    if (backward && vec && a.tpr >= 32) {
+        const int inputs = a.x ? 3 : 2, rings = block_threads(a.tpr) / a.tpr;
         a.stage_bytes = inputs * a.C * (int)es;
         const int blocks = (int)(resident_blocks(h, backward) / h->nsm), room = (SM_SHARED_BYTES / blocks - BLOCK_SHARED_BYTES) / rings / a.stage_bytes;
         a.stages = room < MAX_STAGES ? room : MAX_STAGES;
