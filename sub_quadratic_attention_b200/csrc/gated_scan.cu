@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
         }
 
         float h0[V];
-        fine = plain && !ends;
+        fine = plain && !(packed && ends);
         {
             float gp[V], gq[V], state[V];
             get(&sP[group][lane * V], gp);
@@ -747,6 +747,22 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
                 fine &= finite(h0[j]);
             }
         }
+        auto products = [&](int r, float (&pr)[V]) {
+            if constexpr (KEPT) M::kept(pg, pv, r, pr);
+            else if constexpr (M::ON) fill(pr, head_P[r][threadIdx.x]);
+            else spread(pr, P[r]);
+        };
+        if (!packed && ends && p.a.hT && rows.mine) {
+            // the state behind a dense sequence's last row, by the thread that has the row
+#pragma unroll
+            for (int r = 0; r < S::ROWS; r++)
+                if (rows.t0 + r == p.a.L - 1) {
+                    float pr[V];
+                    products(r, pr);
+#pragma unroll
+                    for (int j = 0; j < V; j++) p.a.hT[(long long)at.b * p.C + c + j] = fma0(pr[j], h0[j], Q[r][j]);
+                }
+        }
         auto finish = [&](auto careful) {
             constexpr bool CARE = decltype(careful)::value;
             TV *y = rows.template first<TV>(p.a.y, c);
@@ -754,9 +770,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
             for (int r = 0; r < S::ROWS; r++) {
                 if (CARE && r >= rows.count) break;
                 float h[V], pr[V];
-                if constexpr (KEPT) M::kept(pg, pv, r, pr);
-                else if constexpr (M::ON) fill(pr, head_P[r][threadIdx.x]);
-                else spread(pr, P[r]);
+                products(r, pr);
                 if constexpr (CARE) {
 #pragma unroll
                     for (int j = 0; j < V; j++) h[j] = fma0(pr[j], h0[j], Q[r][j]);
@@ -764,11 +778,11 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
                     fma_all(h, pr, h0, Q[r]);
                 }
                 const bool in = !CARE || (rows.t0 + r >= lo && rows.t0 + r < hi);
-                if (CARE && ends && in && p.a.hT) {
-                    const long long n = packed ? marks.last[group * S::ROWS + r] : rows.t0 + r == p.a.L - 1 ? at.b : -1;
+                if (CARE && packed && ends && in && p.a.hT) {
+                    const int n = marks.last[group * S::ROWS + r];
                     if (n >= 0)
 #pragma unroll
-                        for (int j = 0; j < V; j++) p.a.hT[n * p.C + c + j] = h[j];
+                        for (int j = 0; j < V; j++) p.a.hT[(long long)n * p.C + c + j] = h[j];
                 }
                 if (M::ON && (!CARE || whole)) {
                     store<TV, V>(reinterpret_cast<TV *>(pv + M::at_v(r)), h);
@@ -1383,16 +1397,16 @@ size_t workspace(const gated_scan_s *h, long long B, long long L, bool backward)
     return four > one ? four : one;
 }
 
-// Rows that tensor copies can move: 16-byte aligned, with strides that are.
-bool sixteens(const gated_scan_rows &r, size_t es, long long B, long long L) {
-    const auto ok = [&](long long n, long long stride) { return n < 2 || (stride > 0 && stride * es % 16 == 0 && stride * es < (1ull << 40)); };
+// Rows that tensor copies can move: 16-byte aligned, with strides that are, and not into one another.
+bool sixteens(const gated_scan_rows &r, size_t es, long long width, long long B, long long L) {
+    const auto ok = [&](long long n, long long stride) { return n < 2 || (stride >= width && stride * es % 16 == 0 && stride * es < (1ull << 40)); };
     return aligned(r.data, 16) && ok(L, r.row_stride) && ok(B, r.batch_stride);
 }
 int vector_of(const gated_scan_s *h, const gated_scan_args *a, bool backward) {
     const bool head = h->per == GATED_SCAN_PER_HEAD;
     if ((head ? h->D : h->C) % 4 || a->L > 0x7fffffffLL || a->B > 0x7fffffffLL) return 1;
     const size_t ev = elem(h->dtype), eg = elem(h->gate_dtype);
-    const auto ok = [&](const gated_scan_rows &r, size_t es) { return sixteens(r, es, a->B, a->L); };
+    const auto ok = [&](const gated_scan_rows &r, size_t es) { return sixteens(r, es, h->C, a->B, a->L); };
     if (!ok(a->v, ev) || (!head && !ok(a->g, eg))) return 1;
     if (!backward) return ok(a->y, ev) ? 4 : 1;
     return ok(a->dy, ev) && ok(a->dv, ev) && (head || ok(a->dg, eg)) ? 4 : 1;

@@ -188,17 +188,18 @@ def test_broadcast_inputs():
 
 
 @pytest.mark.parametrize("form", ["sigmoid", "exp"])
+@pytest.mark.parametrize("per", ["channel", "head"])
 @pytest.mark.parametrize("low", [-math.inf, torch.finfo(torch.bfloat16).min])
-def test_gates_of_zero_cut(form, low):
+def test_gates_of_zero_cut(form, per, low):
     """A gate of zero takes out all that lies before it, NaN and infinities included, within a chunk and
     across chunks; its gradient there is zero."""
-    g, v, dy, h0, dhT = _inputs(1, 600, 1, 16, "bf16", form, "channel")
+    g, v, dy, h0, dhT = _inputs(1, 600, 1, 16, "bf16", form, per)
     for t in (3, 130, 256, 399, 400):
         g[:, t] = low
     clean = v.clone()
     for t, bad in ((1, math.nan), (129, math.inf), (255, -math.inf), (398, math.nan)):
         v[:, t] = bad
-    with b.GatedScan(1, 16, "bf16", form) as s:
+    with b.GatedScan(1, 16, "bf16", form, per) as s:
         states = s.new_states(1, 600)
         y, hT = s(g.cuda(), v.cuda(), h0=h0.cuda(), states=states)
         dg, dv, dh0 = s.backward(dy.cuda(), g.cuda(), v.cuda(), states, h0=h0.cuda())
@@ -252,6 +253,32 @@ def test_nan_stays_in_its_channel_sequence_and_future():
     assert not bool(torch.isnan(dv).any())
     want[0, 140, 3] = False     # its own gate's slope is the state before it
     assert torch.equal(torch.isnan(dg).cpu(), want)
+
+
+def test_rows_that_overlap():
+    """Windows of one buffer: a row's values begin inside the row before it."""
+    flat_g, flat_v = torch.randn(3000) * 0.5 - 3, torch.randn(3000)
+    g, v = (f.as_strided((2, 150, 32), (1600, 8, 1)) for f in (flat_g, flat_v))
+    dy = torch.randn(2, 150, 32)
+    gd, vd = (f.cuda().as_strided((2, 150, 32), (1600, 8, 1)) for f in (flat_g, flat_v))
+    _check(2, 16, "f32", "sigmoid", "channel", g, v, dy, place=lambda *_: (gd, vd, dy.cuda()))
+
+
+@pytest.mark.parametrize("B,L,H,D,per", [(700, 3, 2, 32, "channel"), (300, 130, 1, 64, "head"), (2, 1, 1, 64, "channel"),
+                                         (600, 128, 1, 64, "channel")])
+def test_many_short_sequences(B, L, H, D, per):
+    """More sequences than blocks: a block takes strip after strip."""
+    g, v, dy, h0, dhT = _inputs(B, L, H, D, "bf16", "sigmoid", per)
+    gd, vd, dyd, h0d, dhTd = _cuda(g, v, dy, h0, dhT)
+    with b.GatedScan(H, D, "bf16", "sigmoid", per) as s:
+        st = s.new_states(B, L)
+        y, hT = s(gd, vd, h0=h0d, states=st)
+        dg, dv, dh0 = s.backward(dyd, gd, vd, st, h0=h0d, dhT=dhTd)
+        torch.cuda.synchronize()
+    pick = torch.tensor([0, 1, B // 2, B - 2, B - 1])
+    val, err = ref.scan(g[pick], v[pick], H, D, "sigmoid", h0[pick], None, dy[pick], dhT[pick])
+    for name, got in (("y", y), ("hT", hT), ("dg", dg), ("dv", dv), ("dh0", dh0)):
+        ref.check(name, got[pick.cuda()], val[name], err[name])
 
 
 def test_empty_calls():

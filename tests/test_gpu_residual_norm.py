@@ -138,6 +138,19 @@ def test_leading_dimensions_and_broadcast_rows():
             n(out.cuda().view(2, 12, 64)[:, :5], x.cuda().view(2, 12, 64)[:, :5], g, be)
 
 
+def test_vectors_at_any_alignment():
+    """gamma and beta may start anywhere: the rows then go value by value."""
+    out, x, dy, gamma, beta = _inputs(13, 64, "f32")
+    g, be = (torch.cat([torch.zeros(1), t]).cuda()[1:] for t in (gamma, beta))
+    with b.ResidualNorm(64, "f32", "post_ln", EPS) as n:
+        y = n(out.cuda(), x.cuda(), g, be)
+        dz, _, dgamma, dbeta = n.backward(dy.cuda(), out.cuda(), x.cuda(), g)
+        torch.cuda.synchronize()
+    val, err = ref.norm(out, x, gamma, beta, "post_ln", EPS, dy)
+    for name, got in (("y", y), ("dz", dz), ("dgamma", dgamma), ("dbeta", dbeta)):
+        ref.check(name, got, val[name], err[name])
+
+
 def test_no_rows():
     with b.ResidualNorm(64, "bf16", "post_ln") as n:
         e = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
