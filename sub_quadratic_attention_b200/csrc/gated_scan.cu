@@ -385,6 +385,8 @@ struct Place {
     __device__ __forceinline__ long long first_word(const Args &p) const { return ((long long)b * p.strips + strip) * p.nchunk; }
 };
 
+constexpr int MANY_SEQUENCES = 1024;   // four to a thread
+
 // Packed rows: the sequence that starts at, and that ends with, each row of the tile (or -1),
 // and the rows that lie in sequences at all.
 struct Marks {
@@ -395,8 +397,17 @@ __device__ __forceinline__ void mark_sequences(const Args &p, Marks &m, long lon
     __syncthreads();   // the last tile's marks have been read
     for (int i = threadIdx.x; i < CHUNK; i += blockDim.x) m.first[i] = m.last[i] = -1;
     __syncthreads();
-    for (long long n = threadIdx.x; n < p.nseq; n += blockDim.x) {
+    // of many sequences the tile's are found first: every stride-th tells which have ended before it
+    const bool many = p.nseq > MANY_SEQUENCES;
+    long long n = threadIdx.x;
+    if (many) {
+        const long long stride = (p.nseq + blockDim.x - 1) / blockDim.x, at = threadIdx.x * stride;
+        const int ended = __syncthreads_count(at < p.nseq && cu[at + 1] <= t0);
+        n += ended ? (ended - 1) * stride : 0;
+    }
+    for (; n < p.nseq; n += blockDim.x) {
         const long long s = cu[n], e = cu[n + 1];
+        if (many && s >= t0 + CHUNK) break;
         if (s >= e) continue;
         if (s >= t0 && s < t0 + CHUNK) m.first[s - t0] = (int)n;
         if (e > t0 && e <= t0 + CHUNK) m.last[e - 1 - t0] = (int)n;
@@ -1506,7 +1517,7 @@ int run(gated_scan_s *h, const gated_scan_args *a, bool backward, void *stream) 
     // tiles are counted in 31 bits, and every index stays well inside 63
     if (a->L > (1LL << 40) || a->B > (1LL << 31) || nseq > (1LL << 40) / h->C) return SPECTRE_ERR_ARG;
     const long long nchunk = (a->L + CHUNK - 1) / CHUNK;
-    if (nchunk && nchunk * a->B > 0x7fffffffLL / strips_of(h, 1)) return SPECTRE_ERR_ARG;
+    if (nchunk > 0x7fffffffLL / strips_of(h, 1) / a->B) return SPECTRE_ERR_ARG;
     const int V = vector_of(h, a, backward);
     const Work work = a->L ? work_of(h, a->B, a->L, backward, V) : Work{};
     const size_t ev = elem(h->dtype), eg = elem(h->gate_dtype);

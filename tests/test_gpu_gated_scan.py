@@ -108,6 +108,15 @@ def test_packed_sequences(cu, per, dtype):
     _check(3, 12, dtype, "sigmoid", per, g, v, dy, None, None, cu=cu, gate_dtype="f32")
 
 
+@pytest.mark.parametrize("per", ["channel", "head"])
+def test_thousands_of_sequences(per):
+    """More sequences than a tile looks through one by one: short ones, empty ones, a long one in the middle."""
+    cu = list(range(3, 1200, 1)) + [1200] * 900 + [2000] + list(range(2002, 2790, 2))
+    L = 2800
+    g, v, dy, h0, dhT = _inputs(1, L, 1, 32, "f32", "exp", per, n=len(cu) - 1)
+    _check(1, 32, "f32", "exp", per, g, v, dy, h0, dhT, cu=cu)
+
+
 def test_rows_outside_the_sequences_are_left_as_they_were():
     cu = [10, 130, 270]
     g, v, dy, h0, _ = _inputs(1, 300, 2, 16, "bf16", "exp", "head", n=2)
@@ -532,6 +541,7 @@ def test_refusals():
         assert run(g=(gd.data_ptr() + 1, 320, 16)) == b.SPECTRE_ERR_ALIGN
         assert run(g=(gd.data_ptr(), 320, -16)) == b.SPECTRE_ERR_ARG and run(g=(0, 320, 16)) == b.SPECTRE_ERR_ARG
         assert run(B=-1) == b.SPECTRE_ERR_ARG and run(B=1 << 40, L=1 << 40) == b.SPECTRE_ERR_ARG
+        assert run(B=1 << 31, L=1 << 40) == b.SPECTRE_ERR_ARG and run(B=1 << 31, L=1) == b.SPECTRE_ERR_ARG
     with b.GatedScan(2, 160, "f32", "exp", "head") as s:
         need = b.gated_scan_workspace_bytes(s.handle, 1, 4, True)
         t = [torch.zeros(1, 4, n, device="cuda") for n in (2, 320, 320, 2, 320)]
