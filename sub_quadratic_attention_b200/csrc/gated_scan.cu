@@ -244,6 +244,11 @@ struct Args {
 
 __device__ __forceinline__ int head_of(const Args &p, int c) { return (int)((unsigned)c * p.head_of >> 40); }
 
+// Where batch entry b's state stands in h0 and its like, and the state before its chunk in `states`: more
+// values than 32 bits count where millions of sequences have a thousand channels.
+__device__ __forceinline__ long long end_at(const Args &p, int b) { return (long long)b * p.C; }
+__device__ __forceinline__ long long state_at(const Args &p, int b, int chunk) { return ((long long)b * p.nchunk + chunk) * p.C; }
+
 template <typename T> __device__ __forceinline__ T *row(const gated_scan_rows &r, long long b, long long t) {
     return static_cast<T *>(r.data) + b * r.batch_stride + t * r.row_stride;
 }
@@ -717,14 +722,14 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
             if (x < S::WIDTH) ahead.state[x] = p.serial ? carry : cx < p.C ? look_near<S::WIDTH>(words + x, at.i) : 0.0f;
             __syncthreads();
         } else {
-            if (x < S::WIDTH) ahead.state[x] = !packed && p.a.h0 && cx < p.C ? p.a.h0[at.b * p.C + cx] : 0.0f;
+            if (x < S::WIDTH) ahead.state[x] = !packed && p.a.h0 && cx < p.C ? p.a.h0[end_at(p, at.b) + cx] : 0.0f;
             __syncthreads();
         }
         if (x < S::WIDTH && cx < p.C) {
             const float state = ahead.state[x];
             carry = fma0(allP, state, allQ);
             if (more) publish(words + (long long)at.i * S::WIDTH + x, 0.0f, carry);
-            if (p.a.states) p.a.states[(at.b * p.nchunk + at.i) * p.C + cx] = state;
+            if (p.a.states) p.a.states[state_at(p, at.b, at.i) + cx] = state;
         }
 
         float h0[V];
@@ -753,7 +758,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
                     float pr[V];
                     products(r, pr);
 #pragma unroll
-                    for (int j = 0; j < V; j++) p.a.hT[(long long)at.b * p.C + c + j] = fma0(pr[j], h0[j], Q[r][j]);
+                    for (int j = 0; j < V; j++) p.a.hT[end_at(p, at.b) + c + j] = fma0(pr[j], h0[j], Q[r][j]);
                 }
         }
         auto finish = [&](auto careful) {
@@ -1044,7 +1049,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
         } else if (x < 2 * S::WIDTH) {
             // each group's result becomes the state ahead of it
             const int y = x - S::WIDTH;
-            float h = cx < p.C ? p.a.states[(at.b * p.nchunk + rows.chunk) * p.C + cx] : 0.0f;
+            float h = cx < p.C ? p.a.states[state_at(p, at.b, rows.chunk) + cx] : 0.0f;
 #pragma unroll
             for (int i = 0; i < S::GROUPS; i++) {
                 float gP;
@@ -1064,7 +1069,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
             if (x < S::WIDTH) ahead.state[x] = p.serial ? carry : cx < p.C ? look_near<S::WIDTH>(words + x, at.i) : 0.0f;
             __syncthreads();
         } else {
-            if (x < S::WIDTH) ahead.state[x] = !packed && p.a.dhT && cx < p.C ? p.a.dhT[(long long)at.b * p.C + cx] : 0.0f;
+            if (x < S::WIDTH) ahead.state[x] = !packed && p.a.dhT && cx < p.C ? p.a.dhT[end_at(p, at.b) + cx] : 0.0f;
             __syncthreads();
         }
         if (x < S::WIDTH && cx < p.C) {
@@ -1237,7 +1242,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
             finish(std::true_type{});
         if (!packed && rows.chunk == 0 && group == 0 && rows.mine && p.a.dh0)
 #pragma unroll
-            for (int j = 0; j < V; j++) p.a.dh0[(long long)at.b * p.C + c + j] = e[j];
+            for (int j = 0; j < V; j++) p.a.dh0[end_at(p, at.b) + c + j] = e[j];
         if (packed && at.i == 0) pass_empty(p, p.a.dhT, p.a.dh0, c0, S::WIDTH);
         if (M::ON) {
             fence_proxy_async();

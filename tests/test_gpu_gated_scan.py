@@ -553,3 +553,33 @@ def test_refusals():
             return b._lib.gated_scan_backward(s.handle, a, None)
         assert back(work.data_ptr(), need - 1) == b.SPECTRE_ERR_ARG
         assert back(work.data_ptr() + 4, need) == b.SPECTRE_ERR_ALIGN
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_states_beyond_32_bits(shared):
+    """More than 2^31 values of h0, hT, states and their gradients: the last sequences' are found, and those on either
+    side of the 2^31st.  ``shared``: inputs of stride 0, which are read value by value."""
+    B, C = (1 << 21) + 5, 1024
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    g = torch.randn(B, 1, 1, generator=gen, device="cuda").bfloat16()
+    rows = [torch.randn(1 if shared else B, 1, C, generator=gen, device="cuda", dtype=torch.bfloat16).expand(B, 1, C) for _ in range(2)]
+    v, dy = rows
+    h0 = torch.randn(B, C, generator=gen, device="cuda")
+    pick = torch.tensor([0, 1, B // 2, (1 << 21) - 1, 1 << 21, B - 2, B - 1])
+    on = pick.cuda()
+    with b.GatedScan(1, C, "bf16", "sigmoid", "head") as s:
+        st = s.new_states(B, 1)
+        y, hT = s(g, v, h0=h0, states=st)
+        assert torch.equal(st[on, 0], h0[on])
+        got = [("y", y[on]), ("hT", hT[on])]
+        del y, hT
+        dg, dv, dh0 = s.backward(dy, g, v, st, h0=h0, dhT=h0)
+        got += [("dg", dg[on]), ("dv", dv[on]), ("dh0", dh0[on])]
+        del dg, dv, dh0, st
+        torch.cuda.synchronize()
+    g, v, dy, h0 = (t[on].cpu() for t in (g, v, dy, h0))
+    val, err = ref.scan(g, v, 1, C, "sigmoid", h0, None, dy, h0)
+    for name, t in got:
+        ref.check(name, t, val[name], err[name])
+    del rows
+    torch.cuda.empty_cache()
