@@ -206,7 +206,9 @@ template <int V, int N> __device__ __forceinline__ void spread(float (&r)[V], co
 }
 template <int FORM> constexpr float HOLD = FORM == GATED_SCAN_EXP ? 1.0f : 0.0f;   // packed: a = 1
 
-// a * h where a factor of zero takes h out, NaN and infinities included
+// a * h where a factor of zero takes h out, NaN and infinities included.  Products of gates are taken so
+// too, each gate cutting off those before it: a NaN that meets a product that is zero already has come into
+// the rows' own result as well, and the next zero takes out both.
 __device__ __forceinline__ float mul0(float a, float h) { return a == 0.0f ? 0.0f : a * h; }
 __device__ __forceinline__ float fma0(float a, float h, float b) { return a == 0.0f ? b : fmaf(a, h, b); }
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < __int_as_float(0x7f800000); }
@@ -650,7 +652,12 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
                     floats(gf, g);
                     floats(vf, v);
                     gates<FORM, FAST>(gf, ka, kc);
-                    mul_all(lastP, lastP, ka);
+                    if constexpr (CARE) {
+#pragma unroll
+                        for (int j = 0; j < GV; j++) lastP[j] = mul0(ka[j], lastP[j]);
+                    } else {
+                        mul_all(lastP, lastP, ka);
+                    }
                     float a[V], c[V];
                     spread(a, ka);
                     spread(c, kc);
@@ -676,13 +683,16 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
         };
         bool arrived = true;
         if (M::ON) arrived = mbar_wait(smem_u32(&bars[turn]), phase, COPY_POLLS * 1000);
-        // Without care a NaN or infinity anywhere leaves the last row without a finite value: then
-        // the rows are walked again.
+        // Without care a NaN or infinity anywhere leaves the last row without a finite value, or the
+        // gates' product (an infinite decay of nothing is nothing in Q): then the rows are walked again.
         bool fine = plain && arrived;
         if (fine) {
             walk(std::false_type{}, false);
 #pragma unroll
             for (int j = 0; j < V; j++) fine &= finite(Q[S::ROWS - 1][j]);
+            if (FORM == GATED_SCAN_EXP)
+#pragma unroll
+                for (int j = 0; j < GV; j++) fine &= finite(lastP[j]);
         }
         if (!fine) walk(std::true_type{}, plain || !arrived);
         {
@@ -712,7 +722,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
                 sP[i][x] = allP;
                 sQ[i][x] = allQ;
                 allQ = fma0(gP, allQ, gQ);
-                allP *= gP;
+                allP = mul0(gP, allP);
             }
             if (at.i > 0 && more && cx < p.C) publish(words + (long long)at.i * S::WIDTH + x, allP, allQ);
         }
@@ -969,11 +979,13 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
                 float v[V], a[V], b[V];
                 value(careful, r, v);
                 opened(r, a, b);
-                mul_all(P, P, a);
                 if constexpr (CARE) {
+#pragma unroll
+                    for (int j = 0; j < V; j++) P[j] = mul0(a[j], P[j]);
 #pragma unroll
                     for (int j = 0; j < V; j++) Q[j] = fma0(a[j], Q[j], FORM == GATED_SCAN_EXP ? v[j] : mul0(b[j], v[j]));
                 } else {
+                    mul_all(P, P, a);
                     if (FORM == GATED_SCAN_SIGMOID) mul_all(v, b, v);
                     fma_all(Q, a, Q, v);
                 }
@@ -992,7 +1004,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
                 add_all(E, d, E);
                 if constexpr (CARE) {
 #pragma unroll
-                    for (int j = 0; j < V; j++) E[j] = mul0(a[j], E[j]), T[j] *= a[j];
+                    for (int j = 0; j < V; j++) E[j] = mul0(a[j], E[j]), T[j] = mul0(a[j], T[j]);
                 } else {
                     mul_all(E, a, E);
                 }
@@ -1005,7 +1017,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
         if (fine) {
             walk(std::false_type{});
 #pragma unroll
-            for (int j = 0; j < V; j++) fine &= finite(Q[j]) && finite(E[j]);
+            for (int j = 0; j < V; j++) fine &= finite(Q[j]) && finite(E[j]) && (FORM == GATED_SCAN_SIGMOID || finite(P[j]));
         }
         if (!fine) walk(std::true_type{});
 #pragma unroll
@@ -1043,7 +1055,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
                 sR[i][x] = allT;
                 sE[i][x] = allE;
                 allE = fma0(gT, allE, gE);
-                allT *= gT;
+                allT = mul0(gT, allT);
             }
             if (at.i > 0 && more && cx < p.C) publish(words + (long long)at.i * S::WIDTH + x, allT, allE);
         } else if (x < 2 * S::WIDTH) {

@@ -583,3 +583,35 @@ def test_states_beyond_32_bits(shared):
         ref.check(name, t, val[name], err[name])
     del rows
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("p,bad,c", [(1, 3, 6), (8, 10, 16), (5, 50, 77), (100, 120, 128), (100, 120, 130), (128, 140, 256), (120, 260, 290)])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("form,value", [("sigmoid", math.nan), ("exp", math.nan), ("exp", math.inf)])
+@pytest.mark.parametrize("dtype,H,D,per", [("bf16", 1, 64, "channel"), ("bf16", 2, 32, "head"), ("f32", 2, 20, "channel"),
+                                           ("f32", 3, 7, "head"), ("bf16", 1, 21, "channel")])
+def test_nan_gates_stay_between_the_cuts(dtype, H, D, per, form, value, packed, p, bad, c):
+    """A gate of NaN (or an infinite decay) between two gates of zero, or in the second of three sequences: the rows
+    before the first border and from the second on are those of the scan without it, in both directions, wherever the
+    borders lie among a thread's rows, its groups and the tiles."""
+    L, cu = 300, [0, p, c, 300] if packed else None
+    g, v, dy, h0, dhT = _inputs(1, L, H, D, dtype, form, per, n=3 if packed else 1)
+    if not packed:
+        g[:, p] = g[:, c] = -math.inf
+    val, err = ref.scan(g, v, H, D, form, h0, cu, dy, dhT)
+    g[:, bad] = value
+    gd, vd, dyd, h0d, dhTd = _cuda(g, v, dy, h0, dhT)
+    cud = torch.tensor(cu, dtype=torch.int32, device="cuda") if packed else None
+    with b.GatedScan(H, D, dtype, form, per) as s:
+        st = s.new_states(1, L)
+        y, hT = s(gd, vd, h0=h0d, cu_seqlens=cud, states=st)
+        dg, dv, dh0 = s.backward(dyd, gd, vd, st, h0=h0d, dhT=dhTd, cu_seqlens=cud)
+        torch.cuda.synchronize()
+    clean = torch.ones(L, dtype=torch.bool)
+    clean[p:c] = False
+    for name, got in (("y", y), ("dv", dv), ("dg", dg)):
+        ref.check(name, got[:, clean.cuda()], val[name][:, clean], err[name][:, clean])
+    ends = torch.tensor([0, 2] if packed else [0])
+    for name, got in (("hT", hT), ("dh0", dh0)):
+        ref.check(name, got[ends.cuda()], val[name][ends], err[name][ends])
+    assert not bool(torch.isfinite(y[:, bad]).any()) and not bool(torch.isfinite(dv[:, bad - 1]).any())
