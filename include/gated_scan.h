@@ -119,6 +119,7 @@ int gated_scan_run(gated_scan_t h, const gated_scan_args *a, void *stream);
  *   dh_t = dy_t + a_{t+1} dh_{t+1};  dh0 = a_0 dh_0
  *   sigmoid: dv = dh (1 - a), dg = dh (h_{t-1} - v) a (1 - a);
  *   exp:     dv = dh,         dg = dh h_{t-1} a
+ * dg is zero where a (or 1 - a) is, whatever dh and the states are.
  * The states between are recomputed in fp32 from `states`; y is not read.
  */
 int gated_scan_backward(gated_scan_t h, const gated_scan_args *a, void *stream);

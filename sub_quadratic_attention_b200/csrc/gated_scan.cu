@@ -1170,7 +1170,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
 #pragma unroll
                     for (int j = 0; j < V; j++) {
                         dv[j] = !here ? 0.0f : FORM == GATED_SCAN_EXP ? d[j] : mul0(b[j], d[j]);
-                        dg[j] = here ? dg[j] : 0.0f;
+                        dg[j] = here && (FORM == GATED_SCAN_EXP ? a[j] : a[j] * b[j]) != 0.0f ? dg[j] : 0.0f;
                         e[j] = mul0(a[j], d[j]);
                     }
                 } else {

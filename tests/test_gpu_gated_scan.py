@@ -615,3 +615,22 @@ def test_nan_gates_stay_between_the_cuts(dtype, H, D, per, form, value, packed, 
     for name, got in (("hT", hT), ("dh0", dh0)):
         ref.check(name, got[ends.cuda()], val[name][ends], err[name][ends])
     assert not bool(torch.isfinite(y[:, bad]).any()) and not bool(torch.isfinite(dv[:, bad - 1]).any())
+
+
+@pytest.mark.parametrize("form", ["sigmoid", "exp"])
+@pytest.mark.parametrize("dtype,H,D,per", [("bf16", 1, 64, "channel"), ("f32", 3, 7, "head")])
+def test_gradient_of_a_gate_of_zero(dtype, H, D, per, form):
+    """dg has the gate as a factor: where that is zero, dg is zero, though a NaN behind it has reached dh."""
+    L = 300
+    g, v, dy, h0, dhT = _inputs(1, L, H, D, dtype, form, per)
+    cuts = torch.tensor([0, 5, 127, 128, 140, 290])
+    g[:, cuts] = -math.inf
+    g[:, [2, 60, 200, 295]] = math.nan
+    dy[:, [126, 127, 130, 140]] = math.nan
+    gd, vd, dyd, h0d = _cuda(g, v, dy, h0)
+    with b.GatedScan(H, D, dtype, form, per) as s:
+        st = s.new_states(1, L)
+        s(gd, vd, h0=h0d, states=st)
+        dg, _, dh0 = s.backward(dyd, gd, vd, st, h0=h0d)
+        torch.cuda.synchronize()
+    assert not bool(dg[:, cuts.cuda()].any()) and not bool(dh0.any())
