@@ -827,6 +827,83 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
 __host__ __device__ __forceinline__ int first_strip(int h, int D, int width) { return (int)((long long)h * D / width); }
 __host__ __device__ __forceinline__ int last_strip(int h, int D, int width) { return (int)(((long long)h * D + D - 1) / width); }
 
+// A head's gradient at a row, or the part of it that a strip has.
+template <typename TG> __device__ __forceinline__ void put_gate(const Args &p, int b, long long t, int head, int piece, float sum) {
+    if (!p.parts)
+        row<TG>(p.a.dg, b, t)[head] = from_f<TG>(sum);
+    else
+        p.parts[((piece * p.a.B + b) * p.a.L + t) * p.H + head] = sum;
+}
+
+// A thread's rows of a tile without borders, one after another from memory: the state ahead of each is found
+// anew, and a factor of zero takes its operand out.  For rows whose states or gradients overflow between a
+// thread's first and last, which a gate of zero among them must not turn into NaN: so rare that it may be slow,
+// and out of the kernel's way so that it costs few registers there.  Takes the state ahead of the rows and the
+// gradient behind them, returns the gradient ahead.
+template <int V> struct Ends {
+    float h[V], e[V];
+};
+template <typename TV, typename TG, int FORM, bool HEAD, int V>
+__device__ __noinline__ Ends<V> one_by_one(const Args &p, int b, int strip, int chunk, Ends<V> ends, char *pg, char *pv) {
+    using S = Tile<TV, V>;
+    using M = Stage<TV, TG, HEAD, V>;
+    constexpr int GV = HEAD ? 1 : V;
+    const int lane = threadIdx.x % S::LANES, c = strip * S::WIDTH + lane * V, gc = HEAD ? head_of(p, c) : c;
+    const long long t0 = (long long)chunk * CHUNK + threadIdx.x / S::LANES * S::ROWS;
+    const long long count = c < p.C ? p.a.L - t0 : 0;
+    const TG *gp = row<TG>(p.a.g, b, t0) + gc;
+    const TV *vp = row<TV>(p.a.v, b, t0) + c, *dp = row<TV>(p.a.dy, b, t0) + c;
+    auto gate_at = [&](int r, float (&x)[V], float (&y)[V]) {
+        float gf[GV], k[GV], ka[GV], kc[GV];
+        floats(gf, load<TG, GV>(gp + r * p.a.g.row_stride));
+        pack_gates<FORM, sizeof(TV) == 2>(gf, k);
+        open_gates<FORM>(k, ka, kc);
+        spread(x, ka);
+        spread(y, kc);
+    };
+#pragma unroll 1
+    for (int r = S::ROWS - 1; r >= 0; r--) {
+        float sum = 0.0f;
+        if (r < count) {
+            float v[V], x[V], y[V], d[V], dv[V], dg[V], h[V];
+#pragma unroll
+            for (int j = 0; j < V; j++) h[j] = ends.h[j];
+#pragma unroll 1
+            for (int q = 0;; q++) {
+                gate_at(q, x, y);
+                floats(v, load<TV, V>(vp + q * p.a.v.row_stride));
+                if (q == r) break;
+#pragma unroll
+                for (int j = 0; j < V; j++) h[j] = fma0(x[j], h[j], FORM == GATED_SCAN_EXP ? v[j] : mul0(y[j], v[j]));
+            }
+            floats(d, load<TV, V>(dp + r * p.a.dy.row_stride));
+#pragma unroll
+            for (int j = 0; j < V; j++) {
+                const float w = FORM == GATED_SCAN_EXP ? x[j] : x[j] * y[j];
+                d[j] += ends.e[j];
+                dg[j] = w == 0.0f ? 0.0f : w * (FORM == GATED_SCAN_EXP ? h[j] : h[j] - v[j]) * d[j];
+                dv[j] = FORM == GATED_SCAN_EXP ? d[j] : mul0(y[j], d[j]);
+                ends.e[j] = mul0(x[j], d[j]);
+                sum += dg[j];
+            }
+            if constexpr (M::ON) store<TV, V>(reinterpret_cast<TV *>(pv + M::at_v(r)), dv);
+            else store<TV, V>(row<TV>(p.a.dv, b, t0 + r) + c, dv);
+            if constexpr (!HEAD && M::ON) store<TG, V>(reinterpret_cast<TG *>(pg + M::at_g(r)), dg);
+            else if constexpr (!HEAD) store<TG, V>(row<TG>(p.a.dg, b, t0 + r) + c, dg);
+        }
+        if constexpr (HEAD) {
+#pragma unroll
+            for (int o = 0; (1 << o) < S::LANES; o++) {
+                const float other = __shfl_down_sync(0xffffffffu, sum, 1 << o, S::LANES);
+                const int mate = c + (V << o);
+                sum += lane + (1 << o) < S::LANES && mate < p.C && head_of(p, mate) == gc ? other : 0.0f;
+            }
+            if (r < count && (lane == 0 || head_of(p, c - V) != gc)) put_gate<TG>(p, b, t0 + r, gc, strip - first_strip(gc, p.D, S::WIDTH), sum);
+        }
+    }
+    return ends;
+}
+
 constexpr int BACKWARD_BLOCKS = 2;   // an SM: two tiles of three tensors each fill its shared memory
 
 template <typename TV, typename TG, int FORM, bool HEAD, int V>
@@ -1090,18 +1167,18 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
         }
 
         float h[V], e[V];
-        {
+        auto start = [&]() {
             float gt[V], ge[V], grad[V];
             get(&sQ[group][lane * V], h);
             get(&sR[group][lane * V], gt);
             get(&sE[group][lane * V], ge);
             get(&ahead.state[lane * V], grad);
 #pragma unroll
-            for (int j = 0; j < V; j++) {
-                e[j] = fma0(gt[j], grad[j], ge[j]);
-                fine &= finite(h[j]) && finite(e[j]);
-            }
-        }
+            for (int j = 0; j < V; j++) e[j] = fma0(gt[j], grad[j], ge[j]);
+        };
+        start();
+#pragma unroll
+        for (int j = 0; j < V; j++) fine &= finite(h[j]) && finite(e[j]);
         // lanes of one head: lane + 2^o is still in it
         bool same[5], leader = true;
         const bool one_head = HEAD && p.D % S::WIDTH == 0;   // in every strip
@@ -1148,10 +1225,18 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
                     fma_all(h, a, h, v);
                 }
             }
+            // what overflows among the rows stays without a finite value to their end; a held row's distance from
+            // its state is in the slopes alone
+            constexpr bool IN_SLOPES = !CARE && FORM == GATED_SCAN_SIGMOID;
+            if (!CARE)
+#pragma unroll
+                for (int j = 0; j < V; j++) fine &= finite(h[j]);
             asm volatile("" ::: "memory");   // dv goes where the values were
             TV *dv_row = rows.template first<TV>(p.a.dv, c);
             [[maybe_unused]] float head[HEAD ? S::ROWS : 1];
-            TG *dg_row = rows.template first<TG>(p.a.dg, rows.gc);
+            [[maybe_unused]] float all[HEAD ? 1 : V];
+            fill(all, 0.0f);
+            [[maybe_unused]] TG *dg_row = rows.template first<TG>(p.a.dg, rows.gc);
 #pragma unroll
             for (int r = S::ROWS - 1; r >= 0; r--) {
                 const bool here = !CARE || in(r);
@@ -1193,10 +1278,12 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
                         store<TG, V>(reinterpret_cast<TG *>(pg + M::at_g(r)), dg);
                     else if (write)
                         store<TG, V>(dg_row + r * p.a.dg.row_stride, dg);
+                    if constexpr (IN_SLOPES) add_all(all, all, dg);
                 } else {
                     head[r] = 0.0f;
 #pragma unroll
                     for (int j = 0; j < V; j++) head[r] += dg[j];
+                    if constexpr (IN_SLOPES) all[0] += head[r];
                 }
                 if (CARE && edges && here && p.a.dh0) {
                     const long long m = starts(r);
@@ -1205,14 +1292,14 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
                         for (int j = 0; j < V; j++) p.a.dh0[m * p.C + c + j] = e[j];
                 }
             }
+            if constexpr (!CARE)
+#pragma unroll
+                for (int j = 0; j < V; j++) fine &= finite(e[j]) && (!IN_SLOPES || finite(all[HEAD ? 0 : j]));
             if constexpr (HEAD) {
                 // the sums over a head's lanes
                 auto write = [&](int r, float sum) {
                     if (r >= rows.count || (CARE && !in(r) && !p.a.zero_outside)) return;
-                    if (!p.parts)
-                        dg_row[r * p.a.dg.row_stride] = from_f<TG>(sum);
-                    else
-                        p.parts[((piece * p.a.B + at.b) * p.a.L + rows.t0 + r) * p.H + rows.gc] = sum;
+                    put_gate<TG>(p, at.b, rows.t0 + r, rows.gc, piece, sum);
                 };
                 if (one_head) {
                     // halving: each exchange leaves a lane half of its rows, until it has one (or its share of one)
@@ -1248,10 +1335,21 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
             }
         };
         // a warp's lanes sum their heads' gradients together: one way for all of them
-        if (HEAD ? __all_sync(0xffffffffu, fine) : fine)
+        const auto agreed = [&]() { return HEAD ? (bool)__all_sync(0xffffffffu, fine) : fine; };
+        if (agreed()) {
             finish(std::false_type{});
-        else
+            if (!agreed()) {
+                Ends<V> ends;
+                start();
+#pragma unroll
+                for (int j = 0; j < V; j++) ends.h[j] = h[j], ends.e[j] = e[j];
+                ends = one_by_one<TV, TG, FORM, HEAD, V>(p, at.b, at.strip, rows.chunk, ends, pg, pv);
+#pragma unroll
+                for (int j = 0; j < V; j++) e[j] = ends.e[j];
+            }
+        } else {
             finish(std::true_type{});
+        }
         if (!packed && rows.chunk == 0 && group == 0 && rows.mine && p.a.dh0)
 #pragma unroll
             for (int j = 0; j < V; j++) p.a.dh0[end_at(p, at.b) + c + j] = e[j];

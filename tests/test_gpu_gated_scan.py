@@ -634,3 +634,54 @@ def test_gradient_of_a_gate_of_zero(dtype, H, D, per, form):
         dg, _, dh0 = s.backward(dyd, gd, vd, st, h0=h0d)
         torch.cuda.synchronize()
     assert not bool(dg[:, cuts.cuda()].any()) and not bool(dh0.any())
+
+
+@pytest.mark.parametrize("dtype,H,D,per", [("bf16", 1, 64, "channel"), ("f32", 2, 20, "head"), ("f32", 3, 7, "head"), ("bf16", 1, 21, "channel")])
+@pytest.mark.parametrize("at", [8, 16, 128])
+def test_states_that_overflow_end_at_the_cut(dtype, H, D, per, at):
+    """Two rows of the type's lowest value give a state past fp32; a gate of zero behind them takes it out, though
+    neither the rows of one thread nor the state ahead of them show it alone.  The same for gradients going back."""
+    L, C = 300, H * D
+    low = torch.finfo(TYPES[dtype]).min
+    g, v, dy, h0, dhT = _inputs(1, L, H, D, dtype, "exp", per)
+    v[:, at - 1:at + 1] = low           # h is infinite at row `at`
+    g[:, at] = 0.0
+    g[:, at + 1] = -math.inf
+    dy[:, [at + 63, at + 64]] = low     # dh is infinite at row at + 63
+    g[:, at + 64] = 0.0
+    g[:, at + 63] = -math.inf
+    val, err = ref.scan(g, v, H, D, "exp", h0, None, dy, dhT)
+    gd, vd, dyd, h0d, dhTd = _cuda(g, v, dy, h0, dhT)
+    with b.GatedScan(H, D, dtype, "exp", per) as s:
+        st = s.new_states(1, L)
+        y, hT = s(gd, vd, h0=h0d, states=st)
+        dg, dv, dh0 = s.backward(dyd, gd, vd, st, h0=h0d, dhT=dhTd)
+        torch.cuda.synchronize()
+    sure = torch.ones(L, dtype=torch.bool)
+    sure[at - 1:at + 1] = sure[at + 63:at + 65] = False
+    for name, got in (("y", y), ("dv", dv), ("dg", dg)):
+        ref.check(name, got[:, sure.cuda()], val[name][:, sure], err[name][:, sure])
+    ref.check("hT", hT, val["hT"], err["hT"])
+    ref.check("dh0", dh0, val["dh0"], err["dh0"])
+    assert bool((y[:, at] == -math.inf).all()) and not bool(torch.isfinite(dv[:, at + 63]).any())
+    assert not bool(dg[:, [at + 1, at + 63]].any())
+
+
+@pytest.mark.parametrize("dtype,H,D,per", [("bf16", 1, 64, "channel"), ("f32", 2, 20, "head"), ("bf16", 1, 21, "channel")])
+def test_held_rows_far_from_their_state(dtype, H, D, per):
+    """sigmoid, g = infinity, with values of the type's lowest beside states near its largest: the state is held and
+    the gates' gradients are zero, though the difference between the two is past fp32."""
+    L = 200
+    top = torch.finfo(TYPES[dtype]).max
+    g, v, dy, h0, _ = _inputs(1, L, H, D, dtype, "sigmoid", per)
+    g[:, 2:] = math.inf
+    g[:, 1] = -math.inf
+    v[:, 1], v[:, 2:] = top, -top
+    gd, vd, dyd, h0d = _cuda(g, v, dy, h0)
+    with b.GatedScan(H, D, dtype, "sigmoid", per) as s:
+        st = s.new_states(1, L)
+        y, hT = s(gd, vd, h0=h0d, states=st)
+        dg, dv, _ = s.backward(dyd, gd, vd, st, h0=h0d)
+        torch.cuda.synchronize()
+    assert bool((y[:, 1:] == top).all()) and bool((hT == top).all())
+    assert not bool(dg[:, 1:].any()) and not bool(dv[:, 2:].any()) and not bool(torch.isnan(dv).any())
