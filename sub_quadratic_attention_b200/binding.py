@@ -583,22 +583,34 @@ def _check_outputs(outputs, inputs):
             raise ValueError(f"{name} may not be the same memory as {other}")
 
 
-def _stream_for(stream, device, tensors) -> int:
-    """The raw stream of a call.  Where it is not the current one, the tensors are
-    marked as in use on it, so that their memory is not handed out again before
-    the work enqueued there is done."""
-    torch = _torch()
+def _current_stream(device) -> int:
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
+
+
+def _is_other_stream(stream, device) -> bool:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    current = torch._C._cuda_getCurrentRawStream(device.index)
-    raw = stream if isinstance(stream, int) else stream.cuda_stream
-    if raw != current:
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=device)
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
-    return raw
+        return False
+    return (stream if isinstance(stream, int) else stream.cuda_stream) != _current_stream(device)
+
+
+def _on_stream(stream, device, call, *tensors):
+    """call(*tensors) with ``stream`` as the current one.  What the call makes is that
+    stream's memory then: in the caller's stream's own, work enqueued earlier could
+    still be writing.  The caller's tensors are marked as in use on ``stream`` and the
+    results as in use on the caller's, so that neither are handed out too early."""
+    torch = _torch()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        results = call(*tensors)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    for t in results if isinstance(results, tuple) else (results,):
+        if t is not None:
+            t.record_stream(here)
+    return results
 
 
 def gated_scan_create_status(H: int, D: int, gate: int, per: int, dtype: int,
@@ -683,7 +695,8 @@ class GatedScan:
     For training pass ``states=scan.new_states(B, L)`` to the call and to
     :meth:`backward`.  g, v and dy may be slices of wider rows; the plan holds nothing
     of a call, so it may be used on several streams and threads, and inside a graph's
-    capture.  No autograd graph is recorded: backward() is called explicitly.
+    capture.  A call with ``stream=`` runs as if that were the current stream: its inputs
+    must be ready there.  No autograd graph is recorded: backward() is called explicitly.
     """
 
     def __init__(self, H: int, D: int, dtype: str = "bf16", gate: str = "sigmoid",
@@ -721,6 +734,8 @@ class GatedScan:
     def __call__(self, g, v, h0=None, cu_seqlens=None, y=None, hT=None, states=None, stream=None):
         torch = _torch()
         device = self.device
+        if _is_other_stream(stream, device):
+            return _on_stream(stream, device, self, g, v, h0, cu_seqlens, y, hT, states)
         B, L = check_scan_arguments(self.H, self.D, self.per, self.dtype_code, self.gate_code, g, v, device)
         nseq = B if cu_seqlens is None else check_scan_sequences(B, L, cu_seqlens, device)
         if y is not None:
@@ -738,8 +753,7 @@ class GatedScan:
         a = gated_scan_args(B, L, _rows_of("g", g), _rows_of("v", v), _rows_of("y", y),
                             cu_seqlens=_address(cu_seqlens), nseq=nseq, h0=_address(h0), hT=hT.data_ptr(),
                             states=_address(states), work=_address(work), work_bytes=n, zero_outside=made)
-        gated_scan_run(self.handle, a, _stream_for(stream, device,
-                                                   (g, v, h0, cu_seqlens, y, hT, states, work)))
+        gated_scan_run(self.handle, a, _current_stream(device))
         return y, hT
 
     def backward(self, dy, g, v, states, h0=None, dhT=None, cu_seqlens=None, dg=None, dv=None,
@@ -749,6 +763,8 @@ class GatedScan:
         same g, v, h0 and cu_seqlens filled."""
         torch = _torch()
         device = self.device
+        if _is_other_stream(stream, device):
+            return _on_stream(stream, device, self.backward, dy, g, v, states, h0, dhT, cu_seqlens, dg, dv, dh0)
         B, L = check_scan_arguments(self.H, self.D, self.per, self.dtype_code, self.gate_code, g, v,
                                     device, dy=dy, dg=dg, dv=dv)
         nseq = B if cu_seqlens is None else check_scan_sequences(B, L, cu_seqlens, device)
@@ -771,9 +787,7 @@ class GatedScan:
                             dg=_rows_of("dg", dg), dv=_rows_of("dv", dv), cu_seqlens=_address(cu_seqlens),
                             nseq=nseq, h0=_address(h0), dhT=_address(dhT), dh0=_address(dh0),
                             states=states.data_ptr(), work=_address(work), work_bytes=n, zero_outside=made)
-        gated_scan_backward(self.handle, a,
-                            _stream_for(stream, device, (dy, g, v, states, h0, dhT, cu_seqlens,
-                                                         dg, dv, dh0, work)))
+        gated_scan_backward(self.handle, a, _current_stream(device))
         return dg, dv, dh0
 
     def step(self, g, v, state, slots=None, y=None, new_state=None, stream=None):
@@ -784,6 +798,8 @@ class GatedScan:
         outside the pool is skipped: its y is left as it is, or zero where y is made here."""
         torch = _torch()
         device, B, C = self.device, v.shape[0], self.C
+        if _is_other_stream(stream, device):
+            return _on_stream(stream, device, self.step, g, v, state, slots, y, new_state)
         _check_tensor("g", g, (B, self.H if self.per == GATED_SCAN_PER["head"] else C),
                       _torch_dtype(self.gate_code), device)
         _check_tensor("v", v, (B, C), _torch_dtype(self.dtype_code), device)
@@ -806,10 +822,9 @@ class GatedScan:
         (gs, g1), (vs, v1), (ys, y1) = g.stride(), v.stride(), y.stride()
         if (g1 != 1 and g.shape[1] > 1) or (C > 1 and not v1 == y1 == 1):
             raise ValueError("the last dimension of g, v and y must be contiguous")
-        raw = _stream_for(stream, device, (g, v, state, slots, y, new_state))
         _check(_lib.gated_scan_step(self.handle, B, g.data_ptr(), gs, v.data_ptr(), vs, state.data_ptr(), S,
                                     None if slots is None else slots.data_ptr(), y.data_ptr(), ys,
-                                    new_state.data_ptr(), made, raw), "gated_scan_step")
+                                    new_state.data_ptr(), made, _current_stream(device)), "gated_scan_step")
         return y, new_state
 
     def close(self) -> None:
@@ -899,6 +914,8 @@ class ResidualNorm:
 
     def __call__(self, out, x, gamma, beta, y=None, stream=None):
         torch = _torch()
+        if _is_other_stream(stream, self.device):
+            return _on_stream(stream, self.device, self, out, x, gamma, beta, y)
         check_norm_arguments(self.C, self.dtype_code, self.device, (("gamma", gamma), ("beta", beta)),
                              out=out, x=x, y=y)
         C = self.C
@@ -907,14 +924,15 @@ class ResidualNorm:
         else:
             _check_outputs([("y", y)], [("out", out), ("x", x)])
             y_stride = _row_stride("y", y)
-        raw = _stream_for(stream, self.device, (out, x, gamma, beta, y))
         _check(_lib.residual_norm_run(self.handle, x.numel() // C, out.data_ptr(), _row_stride("out", out),
                                       x.data_ptr(), _row_stride("x", x), gamma.data_ptr(), beta.data_ptr(),
-                                      y.data_ptr(), y_stride, raw), "residual_norm_run")
+                                      y.data_ptr(), y_stride, _current_stream(self.device)), "residual_norm_run")
         return y
 
     def backward(self, dy, out, x, gamma, dout=None, dgamma=None, dbeta=None, stream=None):
         torch = _torch()
+        if _is_other_stream(stream, self.device):
+            return _on_stream(stream, self.device, self.backward, dy, out, x, gamma, dout, dgamma, dbeta)
         if self.post and x is None:
             raise ValueError("the post forms' gradient needs x")
         check_norm_arguments(self.C, self.dtype_code, self.device,
@@ -932,12 +950,11 @@ class ResidualNorm:
         T = out.numel() // self.C
         n = residual_norm_workspace_bytes(self.handle, T)
         work = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
-        raw = _stream_for(stream, self.device, (dy, out, x, gamma, dout, dgamma, dbeta, work))
         _check(_lib.residual_norm_backward(
             self.handle, T, dy.data_ptr(), _row_stride("dy", dy), out.data_ptr(), _row_stride("out", out),
             x.data_ptr() if self.post else None, _row_stride("x", x) if self.post else 0, gamma.data_ptr(),
             dout.data_ptr(), _row_stride("dout", dout), dgamma.data_ptr(), dbeta.data_ptr(), _ptr(work), n,
-            raw), "residual_norm_backward")
+            _current_stream(self.device)), "residual_norm_backward")
         return dout, dout if self.post else dy, dgamma, dbeta
 
     def close(self) -> None:

@@ -81,3 +81,33 @@ def test_layer_in_one_graph_with_new_inputs():
             want = layer(*ins)
             torch.cuda.synchronize()
             assert all(torch.equal(p, q) for p, q in zip(outs, want))
+
+
+def test_results_on_another_stream_are_not_in_memory_still_in_use():
+    """What a call with ``stream=`` makes may not lie where work enqueued earlier on the caller's stream, still
+    waiting to run, is about to write: a tensor of a result's size is filled behind a pause of the caller's stream
+    and given back before each call."""
+    B, L, C = 1, 16384, 128
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    g, v, x, dy = (torch.randn(B, L, C, generator=gen, device="cuda").bfloat16() for _ in range(4))
+    w = torch.ones(C, device="cuda")
+    side = torch.cuda.Stream()
+    with b.GatedScan(2, 64) as scan, b.ResidualNorm(C) as n:
+        states = scan.new_states(B, L)
+        rows = [t[0] for t in (g, v)] + [torch.zeros(L, C, device="cuda")]
+        calls = [lambda **k: scan(g, v, states=states, **k), lambda **k: scan.backward(dy, g, v, states, **k),
+                 lambda **k: scan.step(rows[0], rows[1], rows[2], new_state=states.new_empty(L, C), **k),
+                 lambda **k: (n(v, x, w, w, **k),), lambda **k: n.backward(dy, v, x, w, **k)]
+        for call in calls:
+            want = [t for t in call() if t is not None]
+            torch.cuda.synchronize()
+            raw = torch.empty_like(v)
+            for stream in (side, side.cuda_stream):
+                torch.cuda._sleep(100_000_000)
+                raw.fill_(7.0)
+                del raw
+                got = [t for t in call(stream=stream) if t is not None]
+                torch.cuda.synchronize()
+                assert all(torch.equal(p, q) for p, q in zip(want, got))
+                raw = torch.empty_like(v)
+            del raw, want, got
