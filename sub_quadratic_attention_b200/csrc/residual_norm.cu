@@ -417,12 +417,16 @@ long long backward_blocks(const residual_norm_s *h, long long T) {
     return need < most ? need : most;
 }
 
+// An SM's shared memory for the blocks on it, and what a block needs beside its rings.
+constexpr int SM_SHARED_BYTES = 227 * 1024, BLOCK_SHARED_BYTES = 20 * 1024;
+
 template <typename T, int VEC, int EPT, bool RING, bool FULL, bool LN, bool POST>
 cudaError_t launch_backward(const Args &a, int grid, cudaStream_t s) {
     const int threads = block_threads(a.tpr), bytes = RING ? threads / a.tpr * a.stages * a.stage_bytes : 0;
     const auto kernel = norm_backward<T, VEC, EPT, RING, FULL, LN, POST>;
     if (RING) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        // the same for every width: threads with other plans set it at the same time
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM_SHARED_BYTES - BLOCK_SHARED_BYTES);
         if (e != cudaSuccess) return e;
     }
     kernel<<<grid, threads, bytes, s>>>(a);
@@ -458,9 +462,6 @@ template <typename T, int VEC> cudaError_t launch_norm(int norm, const Args &a, 
     default: return launch<T, VEC, false, false>(a, backward, grid, s);
     }
 }
-
-// An SM's shared memory for the blocks on it, and what a block needs beside its rings.
-constexpr int SM_SHARED_BYTES = 227 * 1024, BLOCK_SHARED_BYTES = 20 * 1024;
 
 bool wide(const void *p, long long stride, size_t es) { return aligned(p, 16) && (stride * es) % 16 == 0; }
 

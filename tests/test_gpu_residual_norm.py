@@ -1,6 +1,7 @@
 """The residual norm on the GPU, forward and backward, against the 64-bit reference with its
 derived error bounds (rows_reference.py)."""
 import math
+import threading
 
 import pytest
 import torch
@@ -247,3 +248,43 @@ def test_refusals():
                                                  p[3], work, size, None)
         assert back(w.data_ptr(), need - 1) == b.SPECTRE_ERR_ARG and back(None, need) == b.SPECTRE_ERR_ARG
         assert back(w.data_ptr() + 4, need) == b.SPECTRE_ERR_ALIGN
+
+
+def test_two_threads_with_plans_of_two_widths():
+    """Plans whose backward passes are one kernel with rings of two sizes, called from two threads at a time."""
+    T, calls = 64, 4000
+    widths, codes, made, errors = (1992, 2000), {}, {}, []
+    go = threading.Barrier(2)
+
+    def work(C):
+        try:
+            out, x, dy, gamma, _ = (t.cuda() for t in _inputs(T, C, "bf16", seed=C))
+            stream = torch.cuda.Stream()
+            stream.wait_stream(torch.cuda.current_stream())
+            with b.ResidualNorm(C, "bf16", "post_ln", EPS) as n:
+                dz, dg, db = torch.empty_like(out), torch.empty_like(gamma), torch.empty_like(gamma)
+                size = b.residual_norm_workspace_bytes(n.handle, T)
+                w = torch.empty(size, dtype=torch.uint8, device="cuda")
+                torch.cuda.synchronize()
+                args = (n.handle, T, dy.data_ptr(), C, out.data_ptr(), C, x.data_ptr(), C, gamma.data_ptr(), dz.data_ptr(), C,
+                        dg.data_ptr(), db.data_ptr(), w.data_ptr(), size, stream.cuda_stream)
+                run = b._lib.residual_norm_backward
+                go.wait(timeout=60)
+                codes[C] = [run(*args) for _ in range(calls)]
+                stream.synchronize()
+                made[C] = dz, dg, db
+        except Exception as e:      # an assertion in a thread would go unseen
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(C,)) for C in widths]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for C in widths:
+        assert codes[C] == [b.SPECTRE_OK] * calls
+        out, x, dy, gamma, beta = _inputs(T, C, "bf16", seed=C)
+        val, err = ref.norm(out, x, gamma, beta, "post_ln", EPS, dy)
+        for name, got in zip(("dz", "dgamma", "dbeta"), made[C]):
+            ref.check(name, got, val[name], err[name])
