@@ -62,6 +62,14 @@ typedef struct gated_scan_s *gated_scan_t;
 enum gated_scan_gate { GATED_SCAN_SIGMOID = 0, GATED_SCAN_EXP = 1 };
 enum gated_scan_per { GATED_SCAN_PER_CHANNEL = 0, GATED_SCAN_PER_HEAD = 1 };
 
+enum gated_scan_option {
+    /* 0 (default).  For tests of the failure path only: 1, a block's first wait for copies of rows gives
+     * up at once (it waits for them again before it goes on without them); 2, every wait for the state
+     * ahead of a block of rows does.  Rows that are not aligned for copies have no waits of the first kind,
+     * and sequences that one block takes alone none of the second. */
+    GATED_SCAN_OPT_TEST_WAIT_TIMEOUT = 1,
+};
+
 /* Rows between two saved states (see gated_scan_args.states). */
 #define GATED_SCAN_CHUNK 128
 
@@ -72,6 +80,10 @@ enum gated_scan_per { GATED_SCAN_PER_CHANNEL = 0, GATED_SCAN_PER_HEAD = 1 };
  */
 int gated_scan_create(gated_scan_t *out, int H, int D, int gate, int per, int dtype,
                       int gate_dtype);
+
+/* Set an option (enum gated_scan_option) of later calls; not while another thread uses the
+ * handle.  Returns SPECTRE_OK or SPECTRE_ERR_ARG. */
+int gated_scan_set_option(gated_scan_t h, int option, int value);
 
 /* A tensor of rows: element (b, t, i) is data[b * batch_stride + t * row_stride + i]. */
 typedef struct gated_scan_rows {

@@ -48,6 +48,7 @@ SPECTRE_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 GATED_SCAN_GATE = {"sigmoid": 0, "exp": 1}         # enum gated_scan_gate
 GATED_SCAN_PER = {"channel": 0, "head": 1}         # enum gated_scan_per
+GATED_SCAN_OPT_TEST_WAIT_TIMEOUT = 1               # enum gated_scan_option
 GATED_SCAN_CHUNK = 128                             # rows between two saved states
 
 # every entry point the header declares, with its ctypes signature
@@ -77,6 +78,7 @@ SIGNATURES = {
     "dct_mix_run_host": (_i, [_vp, ctypes.c_longlong] + [_vp] * 4 + [ctypes.c_float] + [_vp] * 4),
     "dct_mix_destroy": (_i, [_vp]),
     "gated_scan_create": (_i, [ctypes.POINTER(_vp)] + [_i] * 6),
+    "gated_scan_set_option": (_i, [_vp, _i, _i]),
     "gated_scan_workspace_bytes": (_sz, [_vp, _ll, _ll, _i]),
     "gated_scan_run": (_i, [_vp, ctypes.c_char_p, _vp]),
     "gated_scan_backward": (_i, [_vp, ctypes.c_char_p, _vp]),
@@ -624,6 +626,10 @@ def gated_scan_create(H: int, D: int, gate: int, per: int, dtype: int, gate_dtyp
     code, h = gated_scan_create_status(H, D, gate, per, dtype, gate_dtype)
     _check(code, "gated_scan_create")
     return h
+
+
+def gated_scan_set_option(h: int, option: int, value: int) -> None:
+    _check(_lib.gated_scan_set_option(h, option, value), "gated_scan_set_option")
 
 
 def gated_scan_workspace_bytes(h: Optional[int], B: int, L: int, backward: bool) -> int:

@@ -51,6 +51,7 @@ struct gated_scan_s {
     int gate, per;
     int dtype, gate_dtype;
     int device, nsm;
+    int test_wait;   // GATED_SCAN_OPT_TEST_WAIT_TIMEOUT
 };
 
 namespace gscan {
@@ -239,6 +240,7 @@ struct Args {
     int nchunk;
     int serial;               // a block takes whole strips
     int nsm;
+    unsigned copy_polls, look_polls;   // after which a wait gives up
     long long nseq;           // dense: B
     unsigned long long *words;   // null where no tile waits for another
     float *parts;             // per-head gradients of heads that span strips: [pieces][B L][H]
@@ -294,10 +296,10 @@ __device__ __forceinline__ float gave_up() {
     return __uint_as_float(0x7fc00000u);
 }
 // The same for one channel by one thread, where few tiles are in flight.
-template <int WIDTH> __device__ __forceinline__ float look_near(const unsigned long long *words, int i) {
+template <int WIDTH> __device__ __forceinline__ float look_near(const unsigned long long *words, int i, unsigned most) {
     const unsigned long long *from = words + (long long)(i - 1) * WIDTH;
     unsigned long long w[REACH];
-    for (unsigned polls = 0; polls < MOST_POLLS; polls++) {
+    for (unsigned polls = 0; polls < most; polls++) {
 #pragma unroll
         for (int j = 0; j < REACH; j++) w[j] = peek(from - j * WIDTH);
         int seen = REACH;
@@ -316,7 +318,7 @@ template <int WIDTH> __device__ __forceinline__ float look_near(const unsigned l
     return gave_up();
 }
 template <int WIDTH, int QS>
-__device__ __forceinline__ void look_back(LookBack<WIDTH, QS> &m, const unsigned long long *words, int i, bool mine) {
+__device__ __forceinline__ void look_back(LookBack<WIDTH, QS> &m, const unsigned long long *words, int i, bool mine, unsigned most) {
     const int x = threadIdx.x % WIDTH, q = threadIdx.x / WIDTH;
     // words ahead of tile 0 belong to others, or to nobody: tile 0's comes before them
     const unsigned long long *from = words + (long long)(i - 1 - q * REACH) * WIDTH + x;
@@ -335,14 +337,14 @@ __device__ __forceinline__ void look_back(LookBack<WIDTH, QS> &m, const unsigned
                 seen = P == (unsigned)(NOTHING >> 32) ? REACH + 1 : P == 0 ? j : seen;
             }
             if (!mine || i - 1 - q * REACH < 0) seen = 0;
-        } while (seen > REACH && ++polls < MOST_POLLS);
+        } while (seen > REACH && ++polls < most);
         m.seen[q][x] = (unsigned char)seen;
         __syncthreads();
         int nearest = 0, at = REACH;   // the word with P = 0: thread nearest's number at
         while (nearest < QS && (at = m.seen[nearest][x]) == REACH) nearest++;
         found = !__syncthreads_or(at >= REACH);
         if (!found) {
-            if (__syncthreads_or(++polls >= MOST_POLLS)) {
+            if (__syncthreads_or(++polls >= most)) {
                 if (q == 0) m.state[x] = gave_up();
                 __syncthreads();
                 return;
@@ -481,7 +483,7 @@ using spectre::tc::mbar_init;
 using spectre::tc::mbar_wait;
 using spectre::tc::smem_u32;
 
-constexpr uint32_t COPY_POLLS = 4;   // of a millisecond's suspension and more each
+constexpr unsigned COPY_POLLS = 4000;   // of up to a millisecond's suspension each
 
 __device__ __forceinline__ void tensor_in(char *to, const CUtensorMap *map, int c, int t, int b, uint32_t bar) {
     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(to)),
@@ -518,6 +520,55 @@ template <typename TV, typename TG, bool HEAD, int V> struct Rows {
     template <typename T> __device__ T *first(const gated_scan_rows &r, int column) const { return row<T>(r, at.b, t0) + column; }
 };
 
+// The strips that the channels of head h lie in.
+__host__ __device__ __forceinline__ int first_strip(int h, int D, int width) { return (int)((long long)h * D / width); }
+__host__ __device__ __forceinline__ int last_strip(int h, int D, int width) { return (int)(((long long)h * D + D - 1) / width); }
+
+// A head's gradient at a row, or the part of it that a strip has.
+template <typename TG> __device__ __forceinline__ void put_gate(const Args &p, int b, long long t, int head, int piece, float sum) {
+    if (!p.parts)
+        row<TG>(p.a.dg, b, t)[head] = from_f<TG>(sum);
+    else
+        p.parts[((piece * p.a.B + b) * p.a.L + t) * p.H + head] = sum;
+}
+
+// Where a tile's copies do not come in time, the block asks for no more of them and waits for those once again, so
+// that none lands in shared memory that is another block's by then.  Here its threads leave NaN in what the tile
+// and the block's others behind it would have given.
+template <typename TV, typename TG, bool HEAD, int V, bool BACKWARD> __device__ __noinline__ void leave_nan(const Args &p, Place at, Marks &marks) {
+    using S = Tile<TV, V>;
+    const bool packed = p.a.cu_seqlens != nullptr;
+    const float nan = gave_up();
+    for (const Place by(p, gridDim.x); at.i < p.nchunk; at.advance(p, by)) {
+        const Rows<TV, TG, HEAD, V> rows(p, at, BACKWARD);
+        long long lo = 0, hi = p.a.L;
+        if (packed) mark_sequences(p, marks, (long long)rows.chunk * CHUNK, lo, hi);
+#pragma unroll 1
+        for (int r = 0; r < rows.count; r++) {
+            const long long t = rows.t0 + r;
+            const bool in = t >= lo && t < hi;
+            if (!in && !p.a.zero_outside) continue;
+            float f[V];
+            fill(f, in ? nan : 0.0f);
+            store<TV, V>(row<TV>(BACKWARD ? p.a.dv : p.a.y, at.b, t) + rows.c, f);
+            if constexpr (BACKWARD && HEAD) put_gate<TG>(p, at.b, t, rows.gc, at.strip - first_strip(rows.gc, p.D, S::WIDTH), f[0]);
+            else if constexpr (BACKWARD) store<TG, V>(row<TG>(p.a.dg, at.b, t) + rows.c, f);
+        }
+        const int x = threadIdx.x, cx = rows.c0 + x;
+        float *const ends = BACKWARD ? p.a.dh0 : p.a.hT;
+        if (x < S::WIDTH && cx < p.C) {
+            if (!p.serial && at.i + 1 < p.nchunk) publish(p.words + (at.first_word(p) + at.i) * S::WIDTH + x, 0.0f, nan);
+            if (!BACKWARD && p.a.states) p.a.states[state_at(p, at.b, at.i) + cx] = nan;
+            if (ends && !packed && at.i + 1 == p.nchunk) ends[end_at(p, at.b) + cx] = nan;
+            for (int r = 0; ends && packed && r < CHUNK; r++) {
+                const long long n = BACKWARD ? marks.first[r] : marks.last[r];
+                if (n >= 0) ends[n * p.C + cx] = nan;
+            }
+        }
+        if (packed && at.i == 0) pass_empty(p, BACKWARD ? p.a.dhT : p.a.h0, ends, rows.c0, S::WIDTH);
+    }
+}
+
 // Blocks an SM: 80 registers a thread leave room for three of 256 threads.  With two of them 2^20
 // bf16 rows of 512 channels took 941 us, with three 806.
 template <typename TV, bool HEAD> constexpr int FORWARD_BLOCKS = HEAD && sizeof(TV) == 4 ? 5 : 3;
@@ -550,6 +601,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
     float carry = 0.0f;   // serial: a channel's state (or gradient) behind the last tile
 
     const bool agent = threadIdx.x == S::THREADS - 32;   // issues all copies
+    bool lost = false;   // a tile's copies
     auto fetch = [&](const Place &at, int turn) {
         if (!M::ON || !agent || at.i >= p.nchunk) return;
         char *to = buffers + turn * M::INPUT_BYTES;
@@ -682,10 +734,10 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
             }
         };
         bool arrived = true;
-        if (M::ON) arrived = mbar_wait(smem_u32(&bars[turn]), phase, COPY_POLLS * 1000);
+        if (M::ON) arrived = mbar_wait(smem_u32(&bars[turn]), phase, p.copy_polls);
         // Without care a NaN or infinity anywhere leaves the last row without a finite value, or the
         // gates' product (an infinite decay of nothing is nothing in Q): then the rows are walked again.
-        bool fine = plain && arrived;
+        bool fine = plain;
         if (fine) {
             walk(std::false_type{}, false);
 #pragma unroll
@@ -694,18 +746,24 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
 #pragma unroll
                 for (int j = 0; j < GV; j++) fine &= finite(lastP[j]);
         }
-        if (!fine) walk(std::true_type{}, plain || !arrived);
+        if (!fine) walk(std::true_type{}, plain);
         {
             float lp[V], lq[V];
 #pragma unroll
             for (int j = 0; j < V; j++) {
                 lp[j] = lastP[HEAD ? 0 : j];
-                lq[j] = arrived ? Q[S::ROWS - 1][j] : gave_up();
+                lq[j] = Q[S::ROWS - 1][j];
             }
             put(&sP[group][lane * V], lp);
             put(&sQ[group][lane * V], lq);
         }
-        __syncthreads();
+        if (!M::ON) {
+            __syncthreads();
+        } else if (!__syncthreads_and(arrived)) {
+            lost = true;
+            next = now;
+            break;
+        }
 
         if (M::ON && agent) out_read();   // the other buffer's rows of y have left it
         fetch(next, turn ^ 1);
@@ -727,9 +785,9 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
             if (at.i > 0 && more && cx < p.C) publish(words + (long long)at.i * S::WIDTH + x, allP, allQ);
         }
         if (at.i > 0 && far) {
-            look_back(ahead, words, at.i, cx < p.C);
+            look_back(ahead, words, at.i, cx < p.C, p.look_polls);
         } else if (at.i > 0) {
-            if (x < S::WIDTH) ahead.state[x] = p.serial ? carry : cx < p.C ? look_near<S::WIDTH>(words + x, at.i) : 0.0f;
+            if (x < S::WIDTH) ahead.state[x] = p.serial ? carry : cx < p.C ? look_near<S::WIDTH>(words + x, at.i, p.look_polls) : 0.0f;
             __syncthreads();
         } else {
             if (x < S::WIDTH) ahead.state[x] = !packed && p.a.h0 && cx < p.C ? p.a.h0[end_at(p, at.b) + cx] : 0.0f;
@@ -821,18 +879,10 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
         }
     }
     if (M::ON && agent) out_done();
-}
-
-// The strips that the channels of head h lie in.
-__host__ __device__ __forceinline__ int first_strip(int h, int D, int width) { return (int)((long long)h * D / width); }
-__host__ __device__ __forceinline__ int last_strip(int h, int D, int width) { return (int)(((long long)h * D + D - 1) / width); }
-
-// A head's gradient at a row, or the part of it that a strip has.
-template <typename TG> __device__ __forceinline__ void put_gate(const Args &p, int b, long long t, int head, int piece, float sum) {
-    if (!p.parts)
-        row<TG>(p.a.dg, b, t)[head] = from_f<TG>(sum);
-    else
-        p.parts[((piece * p.a.B + b) * p.a.L + t) * p.H + head] = sum;
+    if (M::ON && lost) {
+        if (agent) mbar_wait(smem_u32(&bars[turn]), phase, COPY_POLLS);
+        leave_nan<TV, TG, HEAD, V, false>(p, next, marks);
+    }
 }
 
 // A thread's rows of a tile without borders, one after another from memory: the state ahead of each is found
@@ -931,6 +981,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
     float carry = 0.0f;   // serial: a channel's state (or gradient) behind the last tile
 
     const bool agent = threadIdx.x == S::THREADS - 32;   // issues all copies
+    bool lost = false;   // a tile's copies
     auto fetch = [&](const Place &at, int turn) {
         if (!M::ON || !agent || at.i >= p.nchunk) return;
         char *to = buffers + turn * TILE_BYTES;
@@ -985,7 +1036,7 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
         auto ends = [&](int r) { return rows.mine ? marks.last[group * S::ROWS + r] : -1; };
 
         bool arrived = true;
-        if (M::ON) arrived = mbar_wait(smem_u32(&bars[turn]), phase, COPY_POLLS * 1000);
+        if (M::ON) arrived = mbar_wait(smem_u32(&bars[turn]), phase, p.copy_polls);
         // the rows' gates stay in registers, values and dy where the copies put them (V = 1: in registers)
         float k[S::ROWS][GV];
         Pack<TV, V> own_v[M::ON ? 1 : S::ROWS], own_d[M::ON ? 1 : S::ROWS];
@@ -1097,8 +1148,6 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
             for (int j = 0; j < V; j++) fine &= finite(Q[j]) && finite(E[j]) && (FORM == GATED_SCAN_SIGMOID || finite(P[j]));
         }
         if (!fine) walk(std::true_type{});
-#pragma unroll
-        for (int j = 0; j < V; j++) E[j] = arrived ? E[j] : gave_up();
         put(&sQ[group][lane * V], Q);
         put(&sR[group][lane * V], T);
         put(&sE[group][lane * V], E);
@@ -1115,7 +1164,13 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
         } else {
             put(&sP[group][lane * V], P);
         }
-        __syncthreads();
+        if (!M::ON) {
+            __syncthreads();
+        } else if (!__syncthreads_and(arrived)) {
+            lost = true;
+            next = now;
+            break;
+        }
 
         if (M::ON && agent) out_read();   // the other buffer's gradients have left it
         fetch(next, turn ^ 1);
@@ -1153,9 +1208,9 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
             }
         }
         if (at.i > 0 && far) {
-            look_back(ahead, words, at.i, cx < p.C);
+            look_back(ahead, words, at.i, cx < p.C, p.look_polls);
         } else if (at.i > 0) {
-            if (x < S::WIDTH) ahead.state[x] = p.serial ? carry : cx < p.C ? look_near<S::WIDTH>(words + x, at.i) : 0.0f;
+            if (x < S::WIDTH) ahead.state[x] = p.serial ? carry : cx < p.C ? look_near<S::WIDTH>(words + x, at.i, p.look_polls) : 0.0f;
             __syncthreads();
         } else {
             if (x < S::WIDTH) ahead.state[x] = !packed && p.a.dhT && cx < p.C ? p.a.dhT[end_at(p, at.b) + cx] : 0.0f;
@@ -1368,6 +1423,10 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
         }
     }
     if (M::ON && agent) out_done();
+    if (M::ON && lost) {
+        if (agent) mbar_wait(smem_u32(&bars[turn]), phase, COPY_POLLS);
+        leave_nan<TV, TG, HEAD, V, true>(p, next, marks);
+    }
 }
 
 // The gate's gradient of heads that span strips: their strips' sums, in order.
@@ -1675,6 +1734,8 @@ int run(gated_scan_s *h, const gated_scan_args *a, bool backward, void *stream) 
     p.head_of = ((1ull << 40) + h->D - 1) / h->D;
     p.strips = strips_of(h, V);
     p.nsm = h->nsm;
+    p.copy_polls = h->test_wait == 1 ? 0 : COPY_POLLS;
+    p.look_polls = h->test_wait == 2 ? 0 : MOST_POLLS;
     p.nchunk = (int)nchunk;
     p.nseq = nseq;
     return status_of(h->gate == GATED_SCAN_EXP ? launch_types<GATED_SCAN_EXP>(h, p, V, backward, work, s)
@@ -1706,7 +1767,7 @@ int gated_scan_create(gated_scan_t *out, int H, int D, int gate, int per, int dt
     int dev = -1, nsm = 0;
     const int st = rows_io::usable_device(&dev, &nsm);
     if (st != SPECTRE_OK) return st;
-    gated_scan_s *h = new (std::nothrow) gated_scan_s{H, D, H * D, gate, per, dtype, gate_dtype, dev, nsm};
+    gated_scan_s *h = new (std::nothrow) gated_scan_s{H, D, H * D, gate, per, dtype, gate_dtype, dev, nsm, 0};
     if (!h) return SPECTRE_ERR_NOMEM;
     *out = h;
     return SPECTRE_OK;
@@ -1760,6 +1821,12 @@ int gated_scan_step(gated_scan_t h, long long B, const void *g, long long g_stri
         return go_shape(bf(), bf(), form);
     };
     return h->gate == GATED_SCAN_EXP ? go_types(std::integral_constant<int, GATED_SCAN_EXP>{}) : go_types(std::integral_constant<int, GATED_SCAN_SIGMOID>{});
+}
+
+int gated_scan_set_option(gated_scan_t h, int option, int value) {
+    if (!h || option != GATED_SCAN_OPT_TEST_WAIT_TIMEOUT || value < 0 || value > 2) return SPECTRE_ERR_ARG;
+    h->test_wait = value;
+    return SPECTRE_OK;
 }
 
 int gated_scan_device_status(gated_scan_t h, void *stream) {

@@ -685,3 +685,81 @@ def test_held_rows_far_from_their_state(dtype, H, D, per):
         torch.cuda.synchronize()
     assert bool((y[:, 1:] == top).all()) and bool((hT == top).all())
     assert not bool(dg[:, 1:].any()) and not bool(dv[:, 2:].any()) and not bool(torch.isnan(dv).any())
+
+
+def _both_ways(s, gd, vd, dyd, h0d, dhTd, cud):
+    st = s.new_states(*vd.shape[:2])
+    y, hT = s(gd, vd, h0=h0d, cu_seqlens=cud, states=st)
+    return dict(y=y, hT=hT, st=st, **dict(zip(("dg", "dv", "dh0"), s.backward(dyd, gd, vd, st, h0=h0d, dhT=dhTd, cu_seqlens=cud))))
+
+
+@pytest.mark.parametrize("B,L,H,D,per,dtype,cu", [(2, 300, 2, 32, "channel", "bf16", None), (1, 9000, 4, 16, "head", "f32", None),
+                                                  (300, 130, 1, 64, "channel", "bf16", None), (1, 700, 1, 320, "head", "bf16", None),
+                                                  (1, 700, 2, 32, "channel", "f32", [3, 3, 128, 400, 400, 690]),
+                                                  (1, 700, 2, 32, "head", "bf16", [0, 129, 129, 600])])
+def test_copies_that_do_not_come_leave_nan(B, L, H, D, per, dtype, cu):
+    """The wait for the copies of rows made to give up while they are on their way: the blocks wait for them again and
+    leave NaN in all that they would have written, the status is reported once, and the next calls are right."""
+    g, v, dy, h0, dhT = _inputs(B, L, H, D, dtype, "sigmoid", per, n=B if cu is None else len(cu) - 1)
+    on = _cuda(g, v, dy, h0, dhT) + [None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")]
+    with b.GatedScan(H, D, dtype, "sigmoid", per) as s:
+        want = _both_ways(s, *on)
+        torch.cuda.synchronize()
+        assert b.gated_scan_device_status(s.handle) == b.SPECTRE_OK
+        b.gated_scan_set_option(s.handle, b.GATED_SCAN_OPT_TEST_WAIT_TIMEOUT, 1)
+        got = _both_ways(s, *on)
+        assert b.gated_scan_device_status(s.handle) == b.SPECTRE_ERR_TIMEOUT
+        assert b.gated_scan_device_status(s.handle) == b.SPECTRE_OK
+        b.gated_scan_set_option(s.handle, b.GATED_SCAN_OPT_TEST_WAIT_TIMEOUT, 0)
+        after = _both_ways(s, *on)
+        torch.cuda.synchronize()
+        assert b.gated_scan_device_status(s.handle) == b.SPECTRE_OK
+    lo, hi = (0, L) if cu is None else (cu[0], cu[-1])
+    for name in ("y", "dg", "dv"):
+        t = got[name].clone()
+        assert bool(torch.isnan(t[:, lo:hi]).all())
+        t[:, lo:hi] = 0
+        assert not bool(t.any())        # rows in no sequence are zero as ever
+    full = torch.ones(h0.shape[0], dtype=torch.bool) if cu is None else torch.tensor([p < q for p, q in zip(cu, cu[1:])])
+    for name, through in (("hT", h0), ("dh0", dhT)):
+        assert bool(torch.isnan(got[name][full.cuda()]).all()) and torch.equal(got[name].cpu()[~full], through[~full])
+    for name in want:
+        assert torch.equal(want[name], after[name]), name
+
+
+@pytest.mark.parametrize("L,H,D,per,dtype", [(1000, 1, 64, "channel", "bf16"), (20000, 1, 64, "channel", "bf16"), (20000, 1, 32, "head", "f32"),
+                                             (1000, 1, 21, "channel", "f32"), (12000, 3, 7, "head", "f32")])
+def test_states_that_do_not_come_leave_nan(L, H, D, per, dtype):
+    """The wait for the state ahead of a block of rows made to give up at once, on either way of looking back: the
+    rows are NaN where it did and right elsewhere, and the status says whether there are any."""
+    g, v, dy, h0, dhT = _inputs(1, L, H, D, dtype, "exp", per, slow=True)
+    on = _cuda(g, v, dy, h0, dhT) + [None]
+    with b.GatedScan(H, D, dtype, "exp", per) as s:
+        want = _both_ways(s, *on)
+        b.gated_scan_set_option(s.handle, b.GATED_SCAN_OPT_TEST_WAIT_TIMEOUT, 2)
+        st = s.new_states(1, L)
+        y, _ = s(*on[:2], h0=on[3], states=st)
+        forward = b.gated_scan_device_status(s.handle)
+        dg, dv, _ = s.backward(on[2], on[0], on[1], want["st"], h0=on[3], dhT=on[4])
+        backward = b.gated_scan_device_status(s.handle)
+        b.gated_scan_set_option(s.handle, b.GATED_SCAN_OPT_TEST_WAIT_TIMEOUT, 0)
+        after = _both_ways(s, *on)
+        torch.cuda.synchronize()
+        assert b.gated_scan_device_status(s.handle) == b.SPECTRE_OK
+    for status, names, sure in ((forward, dict(y=y), slice(0, 128)), (backward, dict(dg=dg, dv=dv), slice((L - 1) // 128 * 128, L))):
+        for name, t in names.items():
+            bad = torch.isnan(t)
+            assert torch.equal(t[~bad], want[name][~bad]) and not bool(bad[:, sure].any())
+            assert bool(bad.any()) == (status == b.SPECTRE_ERR_TIMEOUT)
+        if L <= 1000:       # one thread a channel does not look before it gives up
+            assert status == b.SPECTRE_ERR_TIMEOUT
+    for name in want:
+        assert torch.equal(want[name], after[name]), name
+
+
+def test_wait_option_is_validated():
+    with b.GatedScan(1, 8, "f32") as s:
+        for option, value in ((b.GATED_SCAN_OPT_TEST_WAIT_TIMEOUT, 3), (b.GATED_SCAN_OPT_TEST_WAIT_TIMEOUT, -1), (0, 1), (2, 0)):
+            with pytest.raises(b.SpectreMixError):
+                b.gated_scan_set_option(s.handle, option, value)
+    assert b._lib.gated_scan_set_option(None, b.GATED_SCAN_OPT_TEST_WAIT_TIMEOUT, 0) == b.SPECTRE_ERR_ARG
