@@ -43,10 +43,21 @@ extern "C" {
 
 typedef struct residual_norm_s *residual_norm_t;
 
+enum residual_norm_option {
+    /* 0 (default).  1, for tests of the failure path only: a wait for copies of rows gives up at once (they
+     * are waited for again before the block goes on without them).  Only the backward pass has such waits,
+     * over rows of more than 128 values that are aligned for copies. */
+    RESIDUAL_NORM_OPT_TEST_WAIT_TIMEOUT = 1,
+};
+
 /* Create a plan for rows of C values on the current CUDA device; norm: enum
  * spectre_norm; eps finite and > 0.  Returns SPECTRE_OK, SPECTRE_ERR_ARG,
  * SPECTRE_ERR_DEVICE (no sm_100 device) or SPECTRE_ERR_NOMEM. */
 int residual_norm_create(residual_norm_t *out, int C, int dtype, int norm, float eps);
+
+/* Set an option (enum residual_norm_option) of later calls; not while another thread uses the
+ * handle.  Returns SPECTRE_OK or SPECTRE_ERR_ARG. */
+int residual_norm_set_option(residual_norm_t h, int option, int value);
 
 /* Enqueue y for T rows on `stream`.  T = 0 does nothing.  Returns SPECTRE_ERR_ARG (a
  * NULL pointer, T < 0, a bad stride), SPECTRE_ERR_ALIGN, SPECTRE_ERR_DEVICE when the
@@ -67,8 +78,8 @@ int residual_norm_backward(residual_norm_t h, long long T, const void *dy, long 
                            void *stream);
 
 /* Synchronise `stream`; SPECTRE_ERR_TIMEOUT if a bounded wait for a copy gave up in any
- * residual norm on the handle's device since the last call (its row is NaN), else
- * SPECTRE_OK.  Clears the record. */
+ * residual norm on the handle's device since the last call (its row, and others that the
+ * block takes behind it, are NaN, and dgamma and dbeta with them), else SPECTRE_OK.  Clears the record. */
 int residual_norm_device_status(residual_norm_t h, void *stream);
 
 /* Release the handle.  NULL-safe; returns SPECTRE_OK. */

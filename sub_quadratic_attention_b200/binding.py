@@ -49,6 +49,7 @@ SPECTRE_NOALLOC_SCRATCH_BYTES = 64 << 20
 GATED_SCAN_GATE = {"sigmoid": 0, "exp": 1}         # enum gated_scan_gate
 GATED_SCAN_PER = {"channel": 0, "head": 1}         # enum gated_scan_per
 GATED_SCAN_OPT_TEST_WAIT_TIMEOUT = 1               # enum gated_scan_option
+RESIDUAL_NORM_OPT_TEST_WAIT_TIMEOUT = 1            # enum residual_norm_option
 GATED_SCAN_CHUNK = 128                             # rows between two saved states
 
 # every entry point the header declares, with its ctypes signature
@@ -86,6 +87,7 @@ SIGNATURES = {
     "gated_scan_device_status": (_i, [_vp, _vp]),
     "gated_scan_destroy": (_i, [_vp]),
     "residual_norm_create": (_i, [ctypes.POINTER(_vp), _i, _i, _i, ctypes.c_float]),
+    "residual_norm_set_option": (_i, [_vp, _i, _i]),
     "residual_norm_run": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _ll, _vp]),
     "residual_norm_workspace_bytes": (_sz, [_vp, _ll]),
     "residual_norm_backward": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _ll, _vp, _vp,
@@ -861,6 +863,10 @@ def residual_norm_create(C: int, dtype: int, norm: int, eps: float = 1e-5) -> in
     code, h = residual_norm_create_status(C, dtype, norm, eps)
     _check(code, "residual_norm_create")
     return h
+
+
+def residual_norm_set_option(h: int, option: int, value: int) -> None:
+    _check(_lib.residual_norm_set_option(h, option, value), "residual_norm_set_option")
 
 
 def residual_norm_workspace_bytes(h: Optional[int], T: int) -> int:

@@ -24,6 +24,7 @@ struct residual_norm_s {
     int C, dtype, norm;
     float eps;
     int device, nsm;
+    int test_wait;   // RESIDUAL_NORM_OPT_TEST_WAIT_TIMEOUT
 };
 
 namespace resnorm {
@@ -46,12 +47,12 @@ struct Args {
     float *part_gamma, *part_beta;   // backward: block i's sums at + i * part_stride
     long long part_stride;
     int stages, stage_bytes;   // of the ring
+    unsigned polls;            // after which a wait for a copy gives up
 };
 
 constexpr int MAX_STAGES = 4;
 constexpr int MAX_RINGS = MIN_THREADS / 32;   // rows of a block that have one: a warp's or wider
-constexpr uint32_t COPY_POLLS = 4000;         // of up to a millisecond's suspension each
-
+constexpr unsigned COPY_POLLS = 4000;         // of up to a millisecond's suspension each
 
 // VEC neighbouring values: one 16-byte access where they are 16 bytes, else one value.
 // Rows pass through once: they leave the first-level cache to gamma and beta.
@@ -129,6 +130,17 @@ using spectre::tc::mbar_init;
 using spectre::tc::mbar_wait;
 using spectre::tc::smem_u32;
 
+// Where a row did not come in time, the thread waits for no more and has NaN for it and those behind it.  The one that
+// asks for them asks for no more either, and waits here for those on their way (rows_left counts from the lost one, of
+// which the block takes every rows-th), so that none lands in shared memory that is another block's by then.
+__device__ __noinline__ void give_up(uint32_t bars, int stage, int stages, uint32_t phase, long long rows_left, long long rows) {
+    atomicExch(&wait_gave_up, 1u);
+    for (int i = 0; i < stages && rows_left > 0; i++, rows_left -= rows) {
+        mbar_wait(bars + 8 * stage, phase, COPY_POLLS);
+        if (++stage == stages) stage = 0, phase ^= 1;
+    }
+}
+
 // A thread's part of a row of N tensors as it stands in memory; columns and rows that do not
 // exist are zero.
 template <typename T, int VEC, int EPT, int N, bool RING> struct Part {
@@ -140,7 +152,8 @@ template <typename T, int VEC, int EPT, int N, bool RING> struct Part {
     uint32_t bars;
     int stages, stage_bytes, stage, bytes;
     uint32_t phase;
-    bool leader;
+    unsigned polls;
+    bool leader, lost;
     __device__ __forceinline__ void begin(int k, const void *p, long long stride, long long r, long long rows, int c) {
         at[k] = static_cast<const T *>(p) + r * stride + (RING ? 0 : c);
         step[k] = rows * stride;
@@ -149,6 +162,8 @@ template <typename T, int VEC, int EPT, int N, bool RING> struct Part {
     __device__ __forceinline__ void open(const Args &a, char *buffers, unsigned long long *all, int group, int lane, long long r, long long rows) {
         stages = a.stages;
         if constexpr (RING) {
+            polls = a.polls;
+            lost = false;
             stage_bytes = a.stage_bytes;
             bytes = a.C * (int)sizeof(T);
             ring = buffers + group * stages * stage_bytes;
@@ -166,7 +181,7 @@ template <typename T, int VEC, int EPT, int N, bool RING> struct Part {
         }
     }
     __device__ __forceinline__ void send(int s, bool there) {
-        if (there && leader) {
+        if (there && leader && !lost) {
             mbar_arrive_expect_tx(bars + 8 * s, N * bytes);
 #pragma unroll
             for (int k = 0; k < N; k++) bulk_copy_g2s(smem_u32(ring + s * stage_bytes) + k * bytes, at[k], bytes, bars + 8 * s);
@@ -174,11 +189,14 @@ template <typename T, int VEC, int EPT, int N, bool RING> struct Part {
 #pragma unroll
         for (int k = 0; k < N; k++) at[k] += step[k];
     }
-    // the row's values, or false where they did not come
-    template <typename M> __device__ __forceinline__ bool fetch(bool there, const M &mine, int c, int apart) {
-        bool came = true;
-        if (RING && there) came = mbar_wait(bars + 8 * stage, phase, COPY_POLLS);
-        if (!came) atomicExch(&wait_gave_up, 1u);
+    // the row's values; rows_left: from it to the end, of which the block takes every rows-th
+    template <typename M> __device__ __forceinline__ void fetch(long long rows_left, long long rows, const M &mine, int c, int apart) {
+        const bool there = rows_left > 0;
+        if constexpr (RING)
+            if (there && !lost && !mbar_wait(bars + 8 * stage, phase, polls)) {
+                lost = true;
+                give_up(bars, stage, stages, phase, leader ? rows_left : 0, rows);
+            }
 #pragma unroll
         for (int k = 0; k < N; k++) {
 #pragma unroll
@@ -195,7 +213,15 @@ template <typename T, int VEC, int EPT, int N, bool RING> struct Part {
             }
             if (!RING) at[k] += step[k];
         }
-        return came;
+        if constexpr (RING)
+            if (there && lost)
+#pragma unroll
+                for (int k = 0; k < N; k++)
+#pragma unroll
+                    for (int i = 0; i < NV; i++)
+                        if (mine[i])
+#pragma unroll
+                            for (int j = 0; j < VEC; j++) v[k][i].v[j] = from_f<T>(__uint_as_float(0x7fc00000u));
     }
     // after every thread of the row has its values: the stage's next row
     __device__ __forceinline__ void pass(bool there) {
@@ -236,9 +262,9 @@ __global__ void __maxnreg__((REGISTERS<EPT, false>)) norm_forward(const __grid_c
     next.begin(1, a.x, a.xs, r, rows, c0);
     T *y = static_cast<T *>(a.y) + r * a.ys + c0;
     constexpr bool EARLY = AHEAD<T, EPT, false>;
-    if (EARLY) next.fetch(r < a.T, mine, c0, apart);
+    if (EARLY) next.fetch(a.T - r, rows, mine, c0, apart);
     for (long long r0 = blockIdx.x * (long long)groups; r0 < a.T; r0 += rows, r += rows, y += rows * a.ys) {
-        if (!EARLY) next.fetch(r < a.T, mine, c0, apart);
+        if (!EARLY) next.fetch(a.T - r, rows, mine, c0, apart);
         Vec<VEC> z[NV], sums(0.0f), squares(0.0f);
         Pack<T, VEC> xr[POST ? 1 : NV];
 #pragma unroll
@@ -248,7 +274,7 @@ __global__ void __maxnreg__((REGISTERS<EPT, false>)) norm_forward(const __grid_c
             else xr[i] = next.v[1][i];
             if (LN) sums = sums + z[i];
         }
-        if (EARLY) next.fetch(r + rows < a.T, mine, c0, apart);
+        if (EARLY) next.fetch(a.T - r - rows, rows, mine, c0, apart);
         Vec<VEC> minus(0.0f);
         if (LN) {
             float s[1] = {sum_of(sums)};
@@ -297,10 +323,9 @@ __global__ void __maxnreg__((REGISTERS<EPT, true>)) norm_backward(const __grid_c
     T *dz = static_cast<T *>(a.y) + r * a.ys + c0;
     next.open(a, buffers, bars, group, lane, r, rows);
     constexpr bool EARLY = AHEAD<T, EPT, RING>;
-    if (EARLY) next.fetch(r < a.T, mine, c0, apart);
+    if (EARLY) next.fetch(a.T - r, rows, mine, c0, apart);
     for (long long r0 = blockIdx.x * (long long)groups; r0 < a.T; r0 += rows, r += rows, dz += rows * a.ys) {
-        bool came = true;
-        if (!EARLY) came = next.fetch(r < a.T, mine, c0, apart);
+        if (!EARLY) next.fetch(a.T - r, rows, mine, c0, apart);
         Vec<VEC> z[NV], dy[NV], sums(0.0f), squares(0.0f), along(0.0f), level(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; i++) {
@@ -309,7 +334,7 @@ __global__ void __maxnreg__((REGISTERS<EPT, true>)) norm_backward(const __grid_c
             if constexpr (POST) z[i] = z[i] + floats(next.v[2][i]);
             if (LN) sums = sums + z[i];
         }
-        if (EARLY) next.fetch(r + rows < a.T, mine, c0, apart);
+        if (EARLY) next.fetch(a.T - r - rows, rows, mine, c0, apart);
         Vec<VEC> minus(0.0f);
         if (LN) {
             float s[1] = {sum_of(sums)};
@@ -330,7 +355,7 @@ __global__ void __maxnreg__((REGISTERS<EPT, true>)) norm_backward(const __grid_c
         float s[3] = {sum_of(squares), sum_of(along), LN ? sum_of(level) : 0.0f};
         row_sums(s, a.tpr, turn);
         next.pass(r + next.stages * rows < a.T);
-        const float rstd = came ? rsqrtf(s[0] * inv + a.eps) : __uint_as_float(0x7fc00000u);   // within two units of the last place
+        const float rstd = rsqrtf(s[0] * inv + a.eps);   // within two units of the last place
         // r (dn - mean(dn) - n mean(dn n)), the means' factors taken together
         const Vec<VEC> scale(rstd), toward(-s[1] * rstd * inv * rstd), off(-s[2] * inv * rstd);
 #pragma unroll
@@ -473,6 +498,7 @@ int enqueue(const residual_norm_s *h, Args &a, bool backward, int grid, cudaStre
     // where they fit.  Loads instead of rings: 65,536 x 512 bf16 69 against 63 us, 49,152 x 2,048 221
     // against 198.  Going forward it is the other way: 33 against 39 us and 112 against 125, for a
     // thread has registers left for the next row and needs no barrier to take it.
+    a.polls = h->test_wait ? 0 : COPY_POLLS;
     a.stages = 0;
     if (backward && vec && a.tpr >= 32) {
         const int inputs = a.x ? 3 : 2, rings = block_threads(a.tpr) / a.tpr;
@@ -507,7 +533,7 @@ int residual_norm_create(residual_norm_t *out, int C, int dtype, int norm, float
     int dev = -1, nsm = 0;
     const int st = rows_io::usable_device(&dev, &nsm);
     if (st != SPECTRE_OK) return st;
-    residual_norm_s *h = new (std::nothrow) residual_norm_s{C, dtype, norm, eps, dev, nsm};
+    residual_norm_s *h = new (std::nothrow) residual_norm_s{C, dtype, norm, eps, dev, nsm, 0};
     if (!h) return SPECTRE_ERR_NOMEM;
     *out = h;
     return SPECTRE_OK;
@@ -601,6 +627,12 @@ int residual_norm_backward(residual_norm_t h, long long T, const void *dy, long 
     config.attrs = &early;
     config.numAttrs = T > 0 ? 1 : 0;
     return status_of(cudaLaunchKernelEx(&config, join_blocks, static_cast<const float *>(part), n, h->C, dgamma, dbeta));
+}
+
+int residual_norm_set_option(residual_norm_t h, int option, int value) {
+    if (!h || option != RESIDUAL_NORM_OPT_TEST_WAIT_TIMEOUT || value < 0 || value > 1) return SPECTRE_ERR_ARG;
+    h->test_wait = value;
+    return SPECTRE_OK;
 }
 
 int residual_norm_device_status(residual_norm_t h, void *stream) {

@@ -288,3 +288,35 @@ def test_two_threads_with_plans_of_two_widths():
         val, err = ref.norm(out, x, gamma, beta, "post_ln", EPS, dy)
         for name, got in zip(("dz", "dgamma", "dbeta"), made[C]):
             ref.check(name, got, val[name], err[name])
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("T,C,dtype", [(5, 512, "bf16"), (3000, 2048, "bf16"), (3000, 200, "bf16"), (700, 8192, "bf16"), (2500, 1000, "f32")])
+def test_copies_that_do_not_come_leave_nan(T, C, dtype, form):
+    """The wait for copies of rows made to give up while they are on their way: they are waited for again, the rows
+    and the weights' gradients are NaN, the status is reported once, and the next calls are right."""
+    if dtype == "f32" and form.startswith("post"):
+        form = form.replace("post", "pre")      # fp32 rows of three inputs are loaded, without a wait
+    out, x, dy, gamma, _ = (t.cuda() for t in _inputs(T, C, dtype))
+    with b.ResidualNorm(C, dtype, form, EPS) as n:
+        want = n.backward(dy, out, x, gamma)
+        torch.cuda.synchronize()
+        assert b.residual_norm_device_status(n.handle) == b.SPECTRE_OK
+        b.residual_norm_set_option(n.handle, b.RESIDUAL_NORM_OPT_TEST_WAIT_TIMEOUT, 1)
+        dz, _, dgamma, dbeta = n.backward(dy, out, x, gamma)
+        assert b.residual_norm_device_status(n.handle) == b.SPECTRE_ERR_TIMEOUT
+        assert b.residual_norm_device_status(n.handle) == b.SPECTRE_OK
+        b.residual_norm_set_option(n.handle, b.RESIDUAL_NORM_OPT_TEST_WAIT_TIMEOUT, 0)
+        after = n.backward(dy, out, x, gamma)
+        torch.cuda.synchronize()
+        assert b.residual_norm_device_status(n.handle) == b.SPECTRE_OK
+    assert all(bool(torch.isnan(t).all()) for t in (dz, dgamma, dbeta))
+    assert all(torch.equal(p, q) for p, q in zip(want, after))
+
+
+def test_wait_option_is_validated():
+    with b.ResidualNorm(512) as n:
+        for option, value in ((b.RESIDUAL_NORM_OPT_TEST_WAIT_TIMEOUT, 2), (b.RESIDUAL_NORM_OPT_TEST_WAIT_TIMEOUT, -1), (0, 1), (2, 0)):
+            with pytest.raises(b.SpectreMixError):
+                b.residual_norm_set_option(n.handle, option, value)
+    assert b._lib.residual_norm_set_option(None, b.RESIDUAL_NORM_OPT_TEST_WAIT_TIMEOUT, 0) == b.SPECTRE_ERR_ARG
