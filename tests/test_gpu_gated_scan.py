@@ -763,3 +763,45 @@ def test_wait_option_is_validated():
             with pytest.raises(b.SpectreMixError):
                 b.gated_scan_set_option(s.handle, option, value)
     assert b._lib.gated_scan_set_option(None, b.GATED_SCAN_OPT_TEST_WAIT_TIMEOUT, 0) == b.SPECTRE_ERR_ARG
+
+
+@pytest.mark.parametrize("per", ["channel", "head"])
+def test_millions_of_sequences(per):
+    """Sequences by the million, most of them of one row and some empty: the blocks that others wait for do not walk
+    them all (that took half a second here; a wait lasts four)."""
+    n, C = 12_000_000, 32
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    lengths = (torch.rand(n, generator=gen, device="cuda") < 0.9).int()
+    lengths[n // 2] = 300
+    cu = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    cu[1:] = lengths.cumsum(0)
+    L = int(cu[-1])
+    g = torch.randn(1, 1, C if per == "channel" else 1, generator=gen, device="cuda").expand(1, L, -1)
+    v, h0 = torch.randn(1, L, C, generator=gen, device="cuda"), torch.randn(n, C, generator=gen, device="cuda")
+    with b.GatedScan(1, C, "f32", "sigmoid", per) as s:
+        st = s.new_states(1, L)
+        calls = [lambda: s(g, v, h0=h0, cu_seqlens=cu, states=st)[1],
+                 lambda: s.backward(v, g, v, st, h0=h0, dhT=h0, cu_seqlens=cu)[2]]
+        ends = []
+        for call in calls:
+            e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            call()
+            e[0].record()
+            ends.append(call())
+            e[1].record()
+            torch.cuda.synchronize()
+            took = e[0].elapsed_time(e[1])
+            assert took < 200.0, took
+        assert b.gated_scan_device_status(s.handle) == b.SPECTRE_OK
+    a = torch.sigmoid(g[0, 0].double())
+    for k in range(0, n, 3_000_000):        # in parts, for their 64-bit copies
+        on = slice(k, k + 3_000_000)
+        empty, one, at = lengths[on] == 0, lengths[on] == 1, cu[on].long()
+        for name, got in zip(("hT", "dh0"), ends):
+            assert torch.equal(got[on][empty], h0[on][empty])
+            row, h = v[0][at[one]].double(), h0[on][one].double()
+            want = a * h + (1 - a) * row if name == "hT" else a * (h + row)
+            off = (got[on][one].double() - want).abs()
+            assert bool((off <= ref.K * ref.U * (h.abs() + row.abs())).all())
+    del v, h0, st, ends
+    torch.cuda.empty_cache()
