@@ -805,3 +805,53 @@ def test_millions_of_sequences(per):
             assert bool((off <= ref.K * ref.U * (h.abs() + row.abs())).all())
     del v, h0, st, ends
     torch.cuda.empty_cache()
+
+
+def _some_channels(H, D, per):
+    """Channels (or whole heads) of the first strip, the middle and the last strip, as (H, D) of their own."""
+    if per == "channel":
+        c = torch.cat([torch.arange(8), torch.arange(8) + H * D // 2, torch.arange(H * D - 40, H * D)])
+        return c, c, len(c), 1
+    heads = torch.tensor([0, H - 1])
+    return heads, (heads[:, None] * D + torch.arange(D)).reshape(-1), 2, D
+
+
+@pytest.mark.parametrize("B,L,H,D,dtype,form,per,cu", [
+    (3, 6001, 10, 64, "bf16", "sigmoid", "channel", None),
+    (3, 6001, 10, 64, "f32", "exp", "head", None),
+    (3, 6001, 16, 128, "bf16", "exp", "head", None),
+    (3, 6001, 10, 64, "f32", "sigmoid", "channel", None),
+    (3, 9001, 7, 33, "bf16", "sigmoid", "channel", None),
+    (2, 12001, 7, 33, "f32", "exp", "head", None),
+    (1, 20003, 10, 64, "bf16", "sigmoid", "channel", [0, 7000, 7000, 7001, 13000, 20003]),
+    (1, 20003, 10, 64, "f32", "exp", "head", [100, 128, 9000, 19999]),
+    (1, 30001, 7, 33, "bf16", "exp", "channel", [0, 15000, 29000]),
+])
+def test_blocks_that_take_tile_after_tile(B, L, H, D, dtype, form, per, cu):
+    """Three tiles a block and more, joined by looking back, over strips, batch entries and chunks: the strips' order,
+    buffers used again and the copies' phases.  Some channels of the first, a middle and the last strip are compared."""
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    C, t, n = H * D, TYPES[dtype], B if cu is None else len(cu) - 1
+    mk = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    z = mk(B, L, C if per == "channel" else H)
+    g = (z * 1.5 + 6 if form == "sigmoid" else -0.003 * torch.nn.functional.softplus(z)).to(t)
+    v, dy = mk(B, L, C).to(t), mk(B, L, C).to(t)
+    h0, dhT = mk(n, C), mk(n, C)
+    cud = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+    with b.GatedScan(H, D, dtype, form, per) as s:
+        got = _both_ways(s, g, v, dy, h0, dhT, cud)
+        torch.cuda.synchronize()
+        assert b.gated_scan_device_status(s.handle) == b.SPECTRE_OK
+    cg, cc, h, d = _some_channels(H, D, per)
+
+    def rows(x, c):     # batch entries beside one another: [1, L, B c]
+        return x.cpu()[:, :, c].transpose(0, 1).reshape(1, L, -1)
+
+    def ends(x):
+        return x.cpu()[:, cc].reshape(1, -1) if cu is None else x.cpu()[:, cc]
+    val, err = ref.scan(rows(g, cg), rows(v, cc), h * B, d, form, ends(h0), cu, rows(dy, cc), ends(dhT))
+    inside = slice(0, L) if cu is None else slice(cu[0], cu[-1])
+    for name, c in (("y", cc), ("dv", cc), ("dg", cg)):
+        ref.check(name, rows(got[name], c)[:, inside], val[name][:, inside], err[name][:, inside])
+    for name in ("hT", "dh0"):
+        ref.check(name, ends(got[name]), val[name], err[name])
