@@ -24,7 +24,10 @@
  * Numbers: v, y, dy and dv are of the plan's dtype, g and dg of its gate dtype
  * (SPECTRE_F32 or SPECTRE_BF16; an fp32 plan has an fp32 gate).  States (h0, hT,
  * dhT, dh0, states, the step's pool) are fp32, and so is all arithmetic; each
- * bf16 output is rounded once, to nearest even.  A run's results do not depend on
+ * bf16 output is rounded once, to nearest even.  The smaller of s(g) and 1 - s(g) is within
+ * 16 * 2^-24 of itself; in the scans of a bf16 plan, which take the hardware's exp2, within
+ * (1.25 |g| + 16) * 2^-24, and zero below 2^-126, so a step's state may differ from a scan's
+ * in its last bits.  A run's results do not depend on
  * how its blocks were scheduled: equal inputs give equal bits.
  *
  * Rows: a tensor of rows is a pointer with a batch stride and a row stride in

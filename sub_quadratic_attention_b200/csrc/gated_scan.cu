@@ -77,9 +77,12 @@ struct Gate {
 // The smaller of a = s(g) and 1 - a = s(-g) is e / (1 + e) with e = exp(-|g|), to its own
 // relative precision; the larger is one minus it, off by at most half a step of one, so that
 // a decay close to one stays as exact as its distance from one.  bf16 rows take the hardware's
-// exp2 and reciprocal (a few units of 2^-24 of the smaller factor, far below the rows' own
-// rounding); a log decay's exp is the accurate one for every type, since its error adds up
-// over as many rows as the state lasts.
+// exp2 and reciprocal.  The exponent g log2(e) is rounded, and log2(e) itself, so the smaller factor is
+// off by up to (1.25 |g| + 10) 2^-24 of itself: 15 units at |g| = 4, 35 at 20, 110 at 80, always far below
+// the rows' own rounding of 2^-8; below 2^-126 (|g| > 87) it is zero.  A second word of the product would
+// take the growth with |g| away for two more operations a gate; where |g| is large the factor is small and
+// its product with it.  A log decay's exp is the accurate one for every type, since its error adds up over
+// as many rows as the state lasts.
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -132,8 +135,8 @@ template <int N, typename T, int V> __device__ __forceinline__ void floats(float
     for (int j = 0; j < V; j++) f[j] = to_f(x.v[j]);
 }
 
-// N gates at once.  For bf16 rows c = 1 / (1 + exp(g)) to its own relative precision, and
-// a = 1 - c, or exp(g) c where that is the smaller.
+// N gates at once.  For bf16 rows c = 1 / (1 + exp(g)), and a = 1 - c, or exp(g) c where that is the
+// smaller: each to the precision of exp (above) relative to itself.
 template <int FORM, bool FAST, int N> __device__ __forceinline__ void gates(const float (&g)[N], float (&a)[N], float (&c)[N]) {
     if constexpr (FORM == GATED_SCAN_SIGMOID && FAST) {
         float k[N], e[N], one[N], d[N], small[N];

@@ -855,3 +855,28 @@ def test_blocks_that_take_tile_after_tile(B, L, H, D, dtype, form, per, cu):
         ref.check(name, rows(got[name], c)[:, inside], val[name][:, inside], err[name][:, inside])
     for name in ("hT", "dh0"):
         ref.check(name, ends(got[name]), val[name], err[name])
+
+
+@pytest.mark.parametrize("C,gate_dtype", [(64, "bf16"), (64, "f32"), (21, "bf16")])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_far_gates_of_bf16_rows(C, gate_dtype, sign):
+    """|g| from 20 to 80, where the hardware's exp2 gets an exponent of up to 115.  Its rounding (u of it) and that of
+    log2(e) (0.23 u) are 1.23 |g| u of the factor; exp2 (4 u), 1 + e (u), the reciprocal (2 u) and a product (u) come to
+    16 u at most.  The fp32 states show it: sums of small factors times values (sign 1, the other factor being one), or
+    the product of one with the state ahead (sign -1, no values)."""
+    L, u = (24, ref.U) if sign > 0 else (1, ref.U)
+    gen = torch.Generator().manual_seed(3)
+    g = (sign * (20 + 60 * torch.rand(1, L, C, generator=gen))).to(TYPES[gate_dtype])
+    v, h0 = torch.randn(1, L, C, generator=gen).bfloat16(), torch.randn(1, C, generator=gen)
+    if sign > 0:
+        h0 = torch.zeros_like(h0)
+    else:
+        v = torch.zeros_like(v)
+    with b.GatedScan(1, C, "bf16", "sigmoid", "channel", gate_dtype) as s:
+        _, hT = s(g.cuda(), v.cuda(), h0=h0.cuda())
+        torch.cuda.synchronize()
+    x = g.double()
+    terms = torch.sigmoid(-x) * v.double() if sign > 0 else torch.sigmoid(x) * h0.double()
+    # 2 L u: a row's addition, and its larger factor, taken as one
+    bound = (terms.abs() * (1.25 * x.abs() + 16 + 2 * L) * u).sum(1)
+    assert bool(((hT.cpu().double() - terms.sum(1)).abs() <= bound).all())
