@@ -462,16 +462,20 @@ template <typename T, int VEC, int EPT, bool LN, bool POST>
 cudaError_t launch_rows(const Args &a, bool backward, int grid, cudaStream_t s) {
     const bool full = VEC > 1 && a.C == a.tpr * EPT;
     if (!backward) {
-        if (full)
-            norm_forward<T, VEC, EPT, true, LN, POST><<<grid, block_threads(a.tpr), 0, s>>>(a);
-        else
-            norm_forward<T, VEC, EPT, false, LN, POST><<<grid, block_threads(a.tpr), 0, s>>>(a);
+        if constexpr (VEC > 1)
+            if (full) {
+                norm_forward<T, VEC, EPT, true, LN, POST><<<grid, block_threads(a.tpr), 0, s>>>(a);
+                return cudaGetLastError();
+            }
+        norm_forward<T, VEC, EPT, false, LN, POST><<<grid, block_threads(a.tpr), 0, s>>>(a);
         return cudaGetLastError();
     }
     if constexpr (VEC > 1)
         if (a.stages)
             return full ? launch_backward<T, VEC, EPT, true, true, LN, POST>(a, grid, s) : launch_backward<T, VEC, EPT, true, false, LN, POST>(a, grid, s);
-    return launch_backward<T, VEC, EPT, false, false, LN, POST>(a, grid, s);
+    // bf16 rows of more than 256 values always have a ring: theirs are 3 * 2 * C bytes a stage at most
+    if constexpr (VEC == 8 && EPT == 16) return cudaErrorInvalidConfiguration;
+    else return launch_backward<T, VEC, EPT, false, false, LN, POST>(a, grid, s);
 }
 
 template <typename T, int VEC, bool LN, bool POST> cudaError_t launch(const Args &a, bool backward, int grid, cudaStream_t s) {
