@@ -575,8 +575,12 @@ template <typename TV, typename TG, bool HEAD, int V, bool BACKWARD> __device__ 
 // Blocks an SM: 80 registers a thread leave room for three of 256 threads.  With two of them 2^20
 // bf16 rows of 512 channels took 941 us, with three 806.
 template <typename TV, bool HEAD> constexpr int FORWARD_BLOCKS = HEAD && sizeof(TV) == 4 ? 5 : 3;
-constexpr int SINGLE_BLOCKS = 3;   // channels one by one, in either direction: 5,003 packed rows of 231 fp32 channels 53 us,
-                                   // with two blocks 64, with four 56
+// Channels one by one, in either direction.  Three blocks spill 100 to 370 bytes a thread going back and are the
+// fastest all the same, at one round of tiles and at many; with two, three and four, forward and backward in us, 231
+// channels: 5,003 packed rows fp32 a decay a head 20.6 + 45.2, 16.5 + 41.2, 16.5 + 42.5; 20,000 rows of the same
+// 31.4 + 93.9, 26.4 + 79.8, 29.1 + 103.6; 65,536 rows, a gate a channel, fp32 90.8 + 249.8, 70.5 + 206.8,
+// 74.4 + 276.1, bf16 77.9 + 236.4, 57.1 + 194.2, 60.9 + 231.2.
+constexpr int SINGLE_BLOCKS = 3;
 
 template <typename TV, typename TG, int FORM, bool HEAD, int V>
 __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS : FORWARD_BLOCKS<TV, HEAD>)
