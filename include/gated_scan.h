@@ -148,7 +148,9 @@ int gated_scan_backward(gated_scan_t h, const gated_scan_args *a, void *stream);
  *   slots     : [B] int32 (device), or NULL: row i has slot i, and S >= B.
  *               A row whose slot is outside [0, S) is skipped: its y is left as it is, or
  *               set to zero with zero_skipped.
- *               Rows that name the same slot are taken in order, one after another.
+ *               Rows that name the same slot are taken in order, one after another.  Every block
+ *               looks through all slots for them, B^2 words in all: no matter to some ten thousand
+ *               rows, but seconds for millions.
  */
 int gated_scan_step(gated_scan_t h, long long B, const void *g, long long g_stride,
                     const void *v, long long v_stride, const float *state, long long S,

@@ -1401,6 +1401,8 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
         if (agreed()) {
             finish(std::false_type{});
             if (!agreed()) {
+                // heads' gradients written so far are written over by other lanes; here all of the warp's come
+                if constexpr (HEAD) __syncwarp();
                 Ends<V> ends;
                 start();
 #pragma unroll
