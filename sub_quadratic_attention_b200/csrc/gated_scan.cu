@@ -20,9 +20,9 @@
 // it, keeps the gates as one number each, and goes back through the rows in the same way.
 //
 // Measured on one B200 (rows of 512 bf16 channels unless said, sigmoid gates a channel):
-// forward 2^20 rows 0.85 ms (3.8 TB/s of 3.2 GB), 131,072 rows 115 us, 64 x 1,024 rows 52
+// forward 2^20 rows 0.83 ms (3.9 TB/s of 3.2 GB), 131,072 rows 115 us, 64 x 1,024 rows 52
 // us; 4 x 12,288 rows of 2,048 fp32 channels, a decay a head, 144 us (5.6 TB/s); backward
-// 131,072 rows 185 us, 4 x 12,288 x 2,048 fp32 221 us (5.5 TB/s).  The same tiles copied
+// 131,072 rows 187 us, 4 x 12,288 x 2,048 fp32 224 us (5.4 TB/s).  The same tiles copied
 // without work take 542 us for 2^20 rows (91% of the copy rate), with the work and no look
 // back 560: what is left is the way of a pair through the second-level cache, about 2 us
 // between publishing and being read with all the others' traffic, and the wait for the
@@ -572,8 +572,9 @@ template <typename TV, typename TG, bool HEAD, int V, bool BACKWARD> __device__ 
     }
 }
 
-// Blocks an SM: 80 registers a thread leave room for three of 256 threads.  With two of them 2^20
-// bf16 rows of 512 channels took 941 us, with three 806.
+// Blocks an SM: 80 registers a thread leave room for three of 256 threads.  With two and with three, bf16 in
+// us: 2^20 rows of 512 channels 930 and 828, 64 x 1,024 rows 58 and 52, 4 x 12,288 rows of 2,048, a decay a
+// head, 132 and 112.
 template <typename TV, bool HEAD> constexpr int FORWARD_BLOCKS = HEAD && sizeof(TV) == 4 ? 5 : 3;
 // Channels one by one, in either direction.  Three blocks spill 100 to 370 bytes a thread going back and are the
 // fastest all the same, at one round of tiles and at many; with two, three and four, forward and backward in us, 231
@@ -602,8 +603,8 @@ __global__ void __launch_bounds__(Tile<TV, V>::THREADS, V == 1 ? SINGLE_BLOCKS :
     Place next(p, blockIdx.x);
     const Place by(p, gridDim.x);
     // more tiles of a strip in flight than one thread's REACH: the whole block looks back.  Where
-    // few are, one thread a channel is enough and asks for less: 64 x 1,024 rows of 512 channels
-    // 51 against 54 us, 4 x 12,288 of 2,048 127 against 137
+    // few are, one thread a channel is enough and asks for less: 64 x 1,024 bf16 rows of 512 channels
+    // 52 against 54 us, back 89 against 94, 4 x 12,288 of 2,048 128 against 136, back 236 against 265
     const bool far = !p.serial && (unsigned)(p.a.B * p.strips) * REACH < gridDim.x;
     float carry = 0.0f;   // serial: a channel's state (or gradient) behind the last tile
 

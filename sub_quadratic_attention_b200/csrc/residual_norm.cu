@@ -501,8 +501,8 @@ int enqueue(const residual_norm_s *h, Args &a, bool backward, int grid, cudaStre
     const bool vec = (h->C * es) % 16 == 0 && wide(a.out, a.outs, es) && wide(a.x, a.xs, es) && wide(a.y, a.ys, es) &&
                      wide(a.dy, a.dys, es) && aligned(a.gamma, 16) && aligned(a.beta, 16);
     // The backward pass's rings: rows of a warp or more, each stage one row of every input; four stages
-    // where they fit.  Loads instead of rings: 65,536 x 512 bf16 69 against 63 us, 49,152 x 2,048 221
-    // against 198.  Going forward it is the other way: 33 against 39 us and 112 against 125, for a
+    // where they fit.  Loads instead of rings: 65,536 x 512 bf16 69 against 61 us, 49,152 x 2,048 221
+    // against 192.  Going forward it is the other way: 33 against 39 us and 112 against 125, for a
     // thread has registers left for the next row and needs no barrier to take it.
     a.polls = h->test_wait ? 0 : COPY_POLLS;
     a.stages = 0;
