@@ -636,7 +636,8 @@ def test_gradient_of_a_gate_of_zero(dtype, H, D, per, form):
     assert not bool(dg[:, cuts.cuda()].any()) and not bool(dh0.any())
 
 
-@pytest.mark.parametrize("dtype,H,D,per", [("bf16", 1, 64, "channel"), ("f32", 2, 20, "head"), ("f32", 3, 7, "head"), ("bf16", 1, 21, "channel")])
+@pytest.mark.parametrize("dtype,H,D,per", [("bf16", 1, 64, "channel"), ("f32", 2, 20, "head"), ("f32", 3, 7, "head"), ("bf16", 1, 21, "channel"),
+                                           ("f32", 32, 3, "head"), ("bf16", 1, 320, "head"), ("bf16", 2, 128, "head")])
 @pytest.mark.parametrize("at", [8, 16, 128])
 def test_states_that_overflow_end_at_the_cut(dtype, H, D, per, at):
     """Two rows of the type's lowest value give a state past fp32; a gate of zero behind them takes it out, though
@@ -667,7 +668,8 @@ def test_states_that_overflow_end_at_the_cut(dtype, H, D, per, at):
     assert not bool(dg[:, [at + 1, at + 63]].any())
 
 
-@pytest.mark.parametrize("dtype,H,D,per", [("bf16", 1, 64, "channel"), ("f32", 2, 20, "head"), ("bf16", 1, 21, "channel")])
+@pytest.mark.parametrize("dtype,H,D,per", [("bf16", 1, 64, "channel"), ("f32", 2, 20, "head"), ("bf16", 1, 21, "channel"), ("f32", 32, 3, "head"),
+                                           ("bf16", 2, 128, "head")])
 def test_held_rows_far_from_their_state(dtype, H, D, per):
     """sigmoid, g = infinity, with values of the type's lowest beside states near its largest: the state is held and
     the gates' gradients are zero, though the difference between the two is past fp32."""
